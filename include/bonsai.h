@@ -45,15 +45,17 @@
  *
  * Conventions for every entry point:
  *   - Pointers are CUDA device pointers (any allocator) and must be 16-byte
- *     aligned; sizes are element counts.  K must be a positive multiple of 128;
- *     M and N must be >= 1 (M = 0 or N = 0 is accepted and launches nothing).
+ *     aligned, unless an entry point says otherwise; sizes are element counts.  K must be a
+ *     positive multiple of 128; M and N must be >= 1 (M = 0 or N = 0 is accepted and
+ *     launches nothing; so are T = 0 and B = 0).
  *   - stream is a cudaStream_t passed as void* (NULL = the legacy default
  *     stream).  Calls are asynchronous on it.  The return value reports argument
  *     validation and launch only: on a non-zero return nothing was launched
  *     (validation) or the launch failed (BONSAI_ERR_CUDA).  Faults inside a
  *     kernel surface at the caller's next synchronisation.
  *   - The library keeps one internal workspace per device (FP32 split-K
- *     partials and an FP16 copy of x' for the prefill GEMM).  It is allocated
+ *     partials, an FP16 copy of x' for the prefill GEMM, the partial results of
+ *     bonsai_paged_attention).  It is allocated
  *     with cudaMalloc on the first call that needs it, grown when a larger
  *     call arrives (after a device synchronisation), and released by
  *     bonsai_shutdown().  Calls that use it must not overlap on the GPU (keep
@@ -95,7 +97,9 @@ typedef enum {
     BONSAI_ERR_ARCH = -6,   /* the current device is not compute capability 10.0  */
     BONSAI_ERR_NOMEM = -7,  /* the internal workspace could not be allocated      */
     BONSAI_ERR_ALGO = -8,   /* the requested kernel cannot run this shape         */
-    BONSAI_ERR_TOO_LARGE = -9 /* beyond the fixed scratch of bonsai_ternary_linear_noalloc */
+    BONSAI_ERR_TOO_LARGE = -9, /* beyond the fixed scratch of bonsai_ternary_linear_noalloc */
+    BONSAI_ERR_ARG = -10    /* an unknown activation, layout, scaling or cache type, or a
+                               parameter outside its range                        */
 } bonsai_status;
 
 /* Kernel selection for bonsai_ternary_linear_algo (bonsai_ternary_linear uses AUTO). */
@@ -204,6 +208,136 @@ int bonsai_swiglu(const uint16_t *y, uint16_t *h, int64_t M, int64_t F, void *st
 int bonsai_ternary_linear_swiglu(const uint16_t *x, const uint8_t *packed, const uint16_t *scales,
                                  uint16_t *h, int64_t M, int64_t F, int64_t K, int fmt, void *stream);
 
+/* Activations of bonsai_ternary_linear_epilogue. */
+typedef enum {
+    BONSAI_ACT_NONE = 0,
+    BONSAI_ACT_RELU = 1,     /* max(z, 0)                                             */
+    BONSAI_ACT_SILU = 2,     /* z / (1 + e^-z)                                        */
+    BONSAI_ACT_GELU = 3,     /* z (1 + erf(z / sqrt 2)) / 2                           */
+    BONSAI_ACT_GELU_TANH = 4 /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2       */
+} bonsai_act;
+
+/* y = act(x' . Wdeq^T + bias) + residual in one call: the product of bonsai_ternary_linear
+ * with its bias, activation and residual stream applied to the FP32 sums, rounded to FP16
+ * once.  bias: N FP16 values, or NULL for none; residual: M x N FP16, or NULL for none; act:
+ * a bonsai_act.  residual may be y itself (the residual stream updated in place) but must
+ * not overlap y otherwise; y must not overlap x, packed, scales or bias.  algo and split_k
+ * choose the kernel as in bonsai_ternary_linear_algo (BONSAI_ALGO_AUTO and 0: the
+ * automatic choice); the GEMM's CTA pairs (split_k = 3) are not available here and return
+ * BONSAI_ERR_ALGO.  An unknown act returns BONSAI_ERR_ARG.  Launches the same kernels as
+ * bonsai_ternary_linear_algo.  A NaN sum (that of a wait that gave up, for instance) stays a
+ * NaN through every activation.  The pages describe no such step: the projections of a decoder
+ * layer add biases and the residual stream here. */
+int bonsai_ternary_linear_epilogue(const uint16_t *x, const uint8_t *packed, const uint16_t *scales,
+                                   const uint16_t *bias, const uint16_t *residual, uint16_t *y, int64_t M,
+                                   int64_t N, int64_t K, int fmt, int act, int algo, int split_k, void *stream);
+
+/* Which elements of a head form the pairs that a rotary position turns: the first R of the
+ * head's D elements are rotated, the rest pass unchanged. */
+typedef enum {
+    BONSAI_ROPE_HALF = 0,       /* (i, i + R/2) for i < R/2 */
+    BONSAI_ROPE_INTERLEAVED = 1 /* (2i, 2i + 1) for i < R/2 */
+} bonsai_rope_layout;
+
+/* How the frequencies of the pairs are stretched for contexts longer than the trained one
+ * (bonsai_rope_frequencies); f_i = base^(-2i/R). */
+typedef enum {
+    BONSAI_ROPE_PLAIN = 0,  /* f_i                                                        */
+    BONSAI_ROPE_LINEAR = 1, /* f_i / factor                                               */
+    BONSAI_ROPE_NTK = 2,    /* f_i with the base times factor^(R / (R - 2))               */
+    BONSAI_ROPE_YARN = 3,   /* f_i / factor for pairs turning fewer than `low` times over
+                               `original` positions, f_i for those turning more than
+                               `high` times, a linear ramp over the pair index between;
+                               magnitude 1 + 0.1 ln(factor)                               */
+    BONSAI_ROPE_BANDS = 4   /* the same two ends, and between them f_i (1 - s) / factor +
+                               f_i s with s linear in the number of turns                 */
+} bonsai_rope_scaling;
+
+/* The frequencies of rotary positions, computed on the HOST in FP64: freqs[i], i < R/2, in
+ * radians per position, and the factor *magnitude on the rotated values (1 but for YARN).
+ * freqs and magnitude are HOST pointers; the caller copies freqs to the device for
+ * bonsai_rope and bonsai_rope_append.  R even and >= 0, base > 1, factor >= 1 (scalings 1 to
+ * 4), original > 0 and 0 < low < high (YARN and BANDS; otherwise ignored); all finite, or
+ * BONSAI_ERR_ARG.  R odd or negative returns BONSAI_ERR_SHAPE.  Needs no GPU. */
+int bonsai_rope_frequencies(double *freqs, double *magnitude, int64_t R, double base, int scaling,
+                            double factor, double original, double low, double high);
+
+/* Rotary positions: turns each pair (a, b) of each head's first R elements by the angle
+ * positions[t] * freqs[i],
+ *   (a, b) -> magnitude * (a cos - b sin, b cos + a sin),
+ * the angle in FP64 (reduced to one turn there, so that far positions lose nothing), the
+ * sine and cosine and the products in FP32, one rounding to FP16.  x and out hold T rows of
+ * H heads of D FP16 elements; row t starts at element t * ld_x (t * ld_out), so that the
+ * query and key heads of a fused projection's output are rotated where they lie.  out may
+ * be x with ld_out = ld_x (in place) but must not overlap it otherwise; elements between
+ * H * D and the row stride are not touched.  freqs: R/2 FP64 values, positions: T int32
+ * values, both device memory aligned to their element.  D a positive multiple of 8 up to
+ * 1024; R even, 0 <= R <= D (R = 0 copies; freqs may then be NULL); ld_x and ld_out at least
+ * H * D and multiples of 8.  No workspace. */
+int bonsai_rope(const uint16_t *x, uint16_t *out, const double *freqs, const int32_t *positions,
+                int64_t T, int64_t H, int64_t D, int64_t R, int64_t ld_x, int64_t ld_out,
+                float magnitude, int layout, void *stream);
+
+/* Element types of a paged key/value cache. */
+typedef enum {
+    BONSAI_KV_F16 = 0, /* FP16                                                             */
+    BONSAI_KV_E4M3 = 1 /* 8-bit floats (4 exponent, 3 mantissa bits) times an FP32 scale per
+                          key/value head: k_scale and v_scale, Hkv values each              */
+} bonsai_kv_type;
+
+/* A paged key/value cache is two pools, k_cache and v_cache, of `pages` pages each:
+ *   pages x Hkv x page_size x D elements of kv_type, row-major,
+ * so that one head's keys of one page are page_size * D contiguous elements.  Position j of
+ * a sequence lies in entry j / page_size of its row of the page table, at place
+ * j % page_size of that page.  page_size is 16, 32, 64, 128 or 256; D 64, 128 or 256;
+ * pages < 2^31.  k_scale and v_scale are read for BONSAI_KV_E4M3 only (NULL otherwise).
+ *
+ * bonsai_rope_append turns one qkv projection's output into the new tokens' queries and
+ * cache entries: row t of qkv (at element t * ld_qkv) holds Hq query heads, Hkv key heads
+ * and Hkv value heads of D elements.  The query heads are rotated as by bonsai_rope into
+ * row t of q_out (at t * ld_q); the key heads are rotated and the value heads copied to
+ * slot slots[t] = page * page_size + place of the pools.  FP16 entries are rounded once
+ * from FP32; E4M3 entries are value / scale, rounded to nearest even and saturated at
+ * +-448 (a NaN stays one).  A negative slot writes no cache entry (a padded row); a slot of
+ * pages * page_size or more writes none either and sets BONSAI_DEVICE_CACHE_RANGE in the
+ * device status word.  Two tokens of one call must not share a slot.  q_out may be qkv with
+ * ld_q = ld_qkv (the query heads then rotated in place) but must not overlap it otherwise.
+ * Hq >= 0, a multiple of Hkv; ld_qkv >= (Hq + 2 Hkv) * D and ld_q >= Hq * D, multiples of
+ * 8; positions (int32), slots (int64), freqs (FP64) and the scales aligned to their
+ * element.  freqs, R, magnitude and layout as for bonsai_rope.  Uses the control words of
+ * the workspace only (the status bit), so it may overlap other calls. */
+int bonsai_rope_append(const uint16_t *qkv, uint16_t *q_out, void *k_cache, void *v_cache,
+                       const float *k_scale, const float *v_scale, const double *freqs,
+                       const int32_t *positions, const int64_t *slots, int64_t T, int64_t Hq, int64_t Hkv,
+                       int64_t D, int64_t R, int64_t ld_qkv, int64_t ld_q, int64_t pages, int64_t page_size,
+                       float magnitude, int layout, int kv_type, void *stream);
+
+/* Attention of one new token per sequence over a paged cache:
+ *   out[b][h] = sum_j p_j v_j,  p = softmax_j(scale * q[b][h] . k_j),
+ * over the positions j of sequence b with max(0, lengths[b] - window) <= j < lengths[b]
+ * (window = 0: all of them; the new token's own entry is appended before the call and
+ * counted in lengths).  Query head h reads key/value head h / (Hq / Hkv).  q and out hold B
+ * rows of Hq heads of D FP16 elements at row strides ld_q and ld_out; out must not overlap
+ * q or the cache.  lse (may be NULL) gets the B x Hq FP32 natural logarithms of the sums of
+ * e^(scale q.k), so that results over parts of a context can be joined.  A sequence of
+ * length 0 gives zeros and an lse of -infinity.
+ *   page_table: B rows of max_pages int32 page numbers; entries past a sequence's last page
+ * (and before its window) are not read.  lengths: B int32 values.  Entries of the cache at
+ * other positions (the rest of the last page, freed pages) are never part of a result,
+ * whatever bits they hold.  A page number outside [0, pages) for a page in use, or a length
+ * that is negative or exceeds max_pages * page_size, makes that sequence's outputs NaN and
+ * sets BONSAI_DEVICE_CACHE_RANGE; nothing outside the buffers is read.
+ *   Statistics, scores and sums are FP32; the probabilities are rounded to FP16 before the
+ * product with the values.  Results depend on the lengths and the device's SM count only
+ * (bitwise repeatable).  Hq a positive multiple of Hkv; ld_q, ld_out at least Hq * D and
+ * multiples of 8; page_table, lengths, lse and the scales aligned to their element; window
+ * >= 0.  Uses the workspace: see the conventions above. */
+int bonsai_paged_attention(const uint16_t *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                           const float *v_scale, const int32_t *page_table, const int32_t *lengths,
+                           uint16_t *out, float *lse, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                           int64_t ld_q, int64_t ld_out, int64_t pages, int64_t page_size, int64_t max_pages,
+                           int64_t window, float scale, int kv_type, void *stream);
+
 /* Number of kernels one bonsai_ternary_linear_algo call with these arguments launches
  * on the current device (the lookup-table GEMV: 1, or 2 when its split-K partials are
  * summed by a second kernel; the integer tensor-core GEMV: 1; the other kernels: 2,
@@ -246,14 +380,16 @@ int bonsai_ternary_linear_noalloc(const uint16_t *x, const uint8_t *packed, cons
                                   uint16_t *y, int64_t M, int64_t N, int64_t K, int fmt, void *stream);
 
 /* Device status bits, set by a kernel whose bounded wait gave up (the call then wrote
- * NaN for the outputs it could not finish; see the conventions above).  They stay set
- * until cleared by bonsai_device_status. */
+ * NaN for the outputs it could not finish; see the conventions above), or that met a slot,
+ * page or length outside the cache.  They stay set until cleared by bonsai_device_status. */
 #define BONSAI_DEVICE_GEMV_COPY_TIMEOUT 1u  /* integer GEMV: a weight copy never landed      */
 #define BONSAI_DEVICE_GEMV_PIECE_TIMEOUT 2u /* integer GEMV: a split tile's later piece, or  */
                                             /* its hand-over, never came                      */
 #define BONSAI_DEVICE_GEMM_TIMEOUT 4u       /* prefill GEMM: a barrier or hand-over wait gave up */
 #define BONSAI_DEVICE_SKINNY_TIMEOUT 8u     /* skinny kernel: the wait after the rotation   */
                                             /* phase, or a weight copy, never ended           */
+#define BONSAI_DEVICE_CACHE_RANGE 16u       /* append or attention: a slot, page or length  */
+                                            /* outside the cache (no such entry was touched)  */
 
 /* Reads the calling device's status bits into *bits after synchronising `stream` (the
  * stream of the calls in question), and clears them when `clear` is non-zero.  *bits is 0

@@ -31,11 +31,13 @@ BONSAI_ERR_ARCH = -6
 BONSAI_ERR_NOMEM = -7
 BONSAI_ERR_ALGO = -8
 BONSAI_ERR_TOO_LARGE = -9
+BONSAI_ERR_ARG = -10
 
 BONSAI_DEVICE_GEMV_COPY_TIMEOUT = 1
 BONSAI_DEVICE_GEMV_PIECE_TIMEOUT = 2
 BONSAI_DEVICE_GEMM_TIMEOUT = 4
 BONSAI_DEVICE_SKINNY_TIMEOUT = 8
+BONSAI_DEVICE_CACHE_RANGE = 16
 
 BONSAI_ALGO_AUTO = 0
 BONSAI_ALGO_SIMPLE = 1
@@ -43,6 +45,24 @@ BONSAI_ALGO_GEMV = 2
 BONSAI_ALGO_SKINNY = 3
 BONSAI_ALGO_GEMM = 4
 BONSAI_ALGO_IMMA = 5
+
+BONSAI_ACT_NONE = 0
+BONSAI_ACT_RELU = 1
+BONSAI_ACT_SILU = 2
+BONSAI_ACT_GELU = 3
+BONSAI_ACT_GELU_TANH = 4
+
+BONSAI_ROPE_HALF = 0
+BONSAI_ROPE_INTERLEAVED = 1
+
+BONSAI_ROPE_PLAIN = 0
+BONSAI_ROPE_LINEAR = 1
+BONSAI_ROPE_NTK = 2
+BONSAI_ROPE_YARN = 3
+BONSAI_ROPE_BANDS = 4
+
+BONSAI_KV_F16 = 0
+BONSAI_KV_E4M3 = 1
 
 FORMATS = {"ptq1": BONSAI_FMT_PTQ1_0, "pq2": BONSAI_FMT_PQ2_0, "q1": BONSAI_FMT_Q1_0,
            "pq2g64": BONSAI_FMT_PQ2_0_G64}
@@ -54,6 +74,7 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 _i64, _int, _p = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
+_f32, _f64 = ctypes.c_float, ctypes.c_double
 
 _SIGS = {
     "bonsai_version": (_int, []),
@@ -71,6 +92,11 @@ _SIGS = {
     "bonsai_launch_count": (_int, [_i64, _i64, _i64, _int, _int, _int]),
     "bonsai_swiglu": (_int, [_p, _p, _i64, _i64, _p]),
     "bonsai_ternary_linear_swiglu": (_int, [_p, _p, _p, _p, _i64, _i64, _i64, _int, _p]),
+    "bonsai_ternary_linear_epilogue": (_int, [_p] * 6 + [_i64] * 3 + [_int] * 4 + [_p]),
+    "bonsai_rope_frequencies": (_int, [_p, _p, _i64, _f64, _int] + [_f64] * 4),
+    "bonsai_rope": (_int, [_p] * 4 + [_i64] * 6 + [_f32, _int, _p]),
+    "bonsai_rope_append": (_int, [_p] * 9 + [_i64] * 9 + [_f32, _int, _int, _p]),
+    "bonsai_paged_attention": (_int, [_p] * 9 + [_i64] * 10 + [_f32, _int, _p]),
     "bonsai_reserve": (_int, [_i64, _i64, _i64]),
     "bonsai_device_status": (_int, [_p, ctypes.POINTER(ctypes.c_uint32), _int]),
     "bonsai_debug_force_timeouts": (_int, [_int]),
@@ -217,6 +243,127 @@ def bonsai_swiglu(y, h, M: int, F: int, stream=None) -> None:
 def bonsai_ternary_linear_swiglu(x, packed, scales, h, M: int, F: int, K: int, fmt: int, stream=None) -> None:
     _check(_lib.bonsai_ternary_linear_swiglu(_ptr(x), _ptr(packed), _ptr(scales), _ptr(h), M, F, K, fmt,
                                              _stream(stream)), "bonsai_ternary_linear_swiglu")
+
+
+_ANY = None  # no dtype or size to check
+
+
+def _dev(t, dtype, numel: int, dev: int, contiguous: bool = True):
+    """Device pointer of a tensor on device `dev`, with the type and at least the size the call
+    reads or writes.  None and plain device pointers pass as they are."""
+    if t is None or type(t) is int:
+        return t
+    if t.get_device() != dev:
+        raise ValueError("tensor arguments must be CUDA tensors on the current device")
+    if t.dtype is not dtype and dtype is not _ANY:
+        raise ValueError(f"a tensor argument is {t.dtype} where {dtype} is expected")
+    if contiguous and not t.is_contiguous():
+        raise ValueError("tensor arguments must be contiguous")
+    if t.numel() < numel:
+        raise ValueError(f"a tensor argument has {t.numel()} elements where the call takes {numel}")
+    return t.data_ptr()
+
+
+def _rows(t, rows: int, width: int, ld, dev: int):
+    """(pointer, row stride) of a matrix of heads: `rows` rows of `width` FP16 elements, at the row
+    stride given or the tensor's own (a contiguous tensor, or a matrix with contiguous rows)."""
+    import torch
+    if t is None or type(t) is int:
+        return t, width if ld is None else ld
+    if ld is None:
+        if t.is_contiguous():
+            ld = t.numel() // rows if rows > 1 else max(width, 8)
+        elif t.dim() == 2 and t.stride(1) == 1:
+            ld = t.stride(0)
+        else:
+            raise ValueError("a strided tensor of heads is a matrix with contiguous rows")
+    if t.dim() == 2 and t.stride(1) == 1 and not t.is_contiguous():
+        if t.shape[0] < rows or t.shape[1] < width or t.stride(0) != ld:
+            raise ValueError("a strided tensor of heads is smaller than the call takes")
+        return _dev(t, torch.float16, 0, dev, False), ld
+    return _dev(t, torch.float16, (rows - 1) * ld + width if rows > 0 else 0, dev), ld
+
+
+def bonsai_ternary_linear_epilogue(x, packed, scales, bias, residual, y, M: int, N: int, K: int, fmt: int,
+                                   act: int = BONSAI_ACT_NONE, algo: int = BONSAI_ALGO_AUTO, split_k: int = 0,
+                                   stream=None) -> None:
+    """y = act(x' . Wdeq^T + bias) + residual; bias and residual may be None, residual may be y."""
+    import torch
+    dev, f16 = torch.cuda.current_device(), torch.float16
+    _check(_lib.bonsai_ternary_linear_epilogue(
+        _dev(x, f16, M * K, dev), _dev(packed, torch.uint8, 0, dev), _dev(scales, f16, 0, dev), _dev(bias, f16, N, dev),
+        _dev(residual, f16, M * N, dev), _dev(y, f16, M * N, dev), M, N, K, fmt, act, algo, split_k, _stream(stream)),
+        "bonsai_ternary_linear_epilogue")
+
+
+def bonsai_rope_frequencies(R: int, base: float, scaling: int = BONSAI_ROPE_PLAIN, factor: float = 1.0,
+                            original: float = 0.0, low: float = 1.0, high: float = 32.0):
+    """(freqs, magnitude): R/2 frequencies in radians per position (an FP64 CPU tensor, to be
+    moved to the device) and the factor on rotated values."""
+    import torch
+    freqs = torch.empty(max(R, 0) // 2, dtype=torch.float64)
+    magnitude = ctypes.c_double(0.0)
+    _check(_lib.bonsai_rope_frequencies(freqs.data_ptr() or None, ctypes.byref(magnitude), R, base, scaling, factor,
+                                        original, low, high), "bonsai_rope_frequencies")
+    return freqs, magnitude.value
+
+
+def bonsai_rope(x, out, freqs, positions, T: int, H: int, D: int, R: int, layout: int = BONSAI_ROPE_HALF,
+                magnitude: float = 1.0, ld_x=None, ld_out=None, stream=None) -> None:
+    """Rotates T rows of H heads of D elements; x and out may be row-strided matrices, out may be x."""
+    import torch
+    dev = torch.cuda.current_device()
+    xp, ld_x = _rows(x, T, H * D, ld_x, dev)
+    op, ld_out = _rows(out, T, H * D, ld_out, dev)
+    _check(_lib.bonsai_rope(xp, op, _dev(freqs, torch.float64, R // 2, dev), _dev(positions, torch.int32, T, dev), T, H, D,
+                            R, ld_x, ld_out, magnitude, layout, _stream(stream)), "bonsai_rope")
+
+
+def _pools(k_cache, v_cache, k_scale, v_scale, dev: int):
+    """Pointers of a pair of cache pools and their scales, and (pages, Hkv, page_size, D, kv_type)."""
+    import torch
+    kind = k_cache.dtype
+    if kind is not torch.float16 and kind is not torch.float8_e4m3fn:
+        raise ValueError("a cache holds float16 or float8_e4m3fn values")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache are two pools of the same shape: pages x Hkv x page_size x D")
+    pages, Hkv, page_size, D = k_cache.shape
+    f32 = torch.float32
+    return ((_dev(k_cache, kind, 0, dev), _dev(v_cache, kind, 0, dev), _dev(k_scale, f32, Hkv, dev),
+             _dev(v_scale, f32, Hkv, dev)),
+            (pages, Hkv, page_size, D, BONSAI_KV_F16 if kind is torch.float16 else BONSAI_KV_E4M3))
+
+
+def bonsai_rope_append(qkv, q_out, k_cache, v_cache, k_scale, v_scale, freqs, positions, slots, T: int, Hq: int,
+                       R: int, layout: int = BONSAI_ROPE_HALF, magnitude: float = 1.0, ld_qkv=None, ld_q=None,
+                       stream=None) -> None:
+    """Rotates the query heads into q_out and the key heads, with the value heads, into the cache pools
+    (pages x Hkv x page_size x D tensors, float16 or float8_e4m3fn with FP32 scales per head)."""
+    import torch
+    dev = torch.cuda.current_device()
+    ptrs, (pages, Hkv, page_size, D, kind) = _pools(k_cache, v_cache, k_scale, v_scale, dev)
+    xp, ld_qkv = _rows(qkv, T, (Hq + 2 * Hkv) * D, ld_qkv, dev)
+    qp, ld_q = _rows(q_out, T, Hq * D, ld_q, dev)
+    _check(_lib.bonsai_rope_append(xp, qp, *ptrs, _dev(freqs, torch.float64, R // 2, dev),
+                                   _dev(positions, torch.int32, T, dev), _dev(slots, torch.int64, T, dev), T, Hq, Hkv, D,
+                                   R, ld_qkv, ld_q, pages, page_size, magnitude, layout, kind, _stream(stream)),
+           "bonsai_rope_append")
+
+
+def bonsai_paged_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, lengths, out, B: int, Hq: int,
+                           window: int = 0, scale=None, lse=None, ld_q=None, ld_out=None, stream=None) -> None:
+    """Attention of one new token per sequence over the cache pools; scale defaults to 1/sqrt(D).
+    page_table is a B x max_pages int32 matrix, lengths B int32 values, lse an optional B x Hq FP32 output."""
+    import torch
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    ptrs, (pages, Hkv, page_size, D, kind) = _pools(k_cache, v_cache, k_scale, v_scale, dev)
+    qp, ld_q = _rows(q, B, Hq * D, ld_q, dev)
+    op, ld_out = _rows(out, B, Hq * D, ld_out, dev)
+    width = page_table.shape[-1]
+    _check(_lib.bonsai_paged_attention(qp, *ptrs, _dev(page_table, i32, B * width, dev), _dev(lengths, i32, B, dev), op,
+                                       _dev(lse, torch.float32, B * Hq, dev), B, Hq, Hkv, D, ld_q, ld_out, pages,
+                                       page_size, width, window, D ** -0.5 if scale is None else scale, kind,
+                                       _stream(stream)), "bonsai_paged_attention")
 
 
 def pack(fmt: int, trits, stream=None):

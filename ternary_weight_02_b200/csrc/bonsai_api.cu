@@ -6,6 +6,7 @@
 // created on first use and kept until bonsai_shutdown().
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <mutex>
 
 #include "../../include/bonsai.h"
@@ -122,6 +123,25 @@ int ensure_workspace(DeviceState &st, size_t data_bytes, size_t zeroed_bytes, Wo
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool aligned_to(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+constexpr int64_t kMaxHeads = 1 << 16, kMaxRopeDim = 1024, kMaxSequences = 1 << 20;
+
+// A row stride of a matrix of heads: rows of `width` elements, 16-byte aligned.
+bool row_stride_ok(int64_t ld, int64_t width) {
+    return ld >= width && ld % 8 == 0 && ld <= (int64_t(1) << 40);
+}
+
+// The shape of a paged cache and of the query heads that use it.
+int check_cache(int64_t Hq, int64_t Hkv, int64_t D, int64_t pages, int64_t page_size, int kv_type) {
+    if (kv_type != BONSAI_KV_F16 && kv_type != BONSAI_KV_E4M3) return BONSAI_ERR_ARG;
+    if (Hkv < 1 || Hkv > kMaxHeads || Hq < 0 || Hq > kMaxHeads || Hq % Hkv != 0) return BONSAI_ERR_SHAPE;
+    if (D != 64 && D != 128 && D != 256) return BONSAI_ERR_SHAPE;
+    if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) != 0) return BONSAI_ERR_SHAPE;
+    if (pages < 1 || pages >= kMaxDim || pages * Hkv >= kMaxDim) return BONSAI_ERR_SHAPE;
+    return BONSAI_OK;
+}
+
 int check_shape(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || N < 0 || K <= 0 || K % kGroup != 0) return BONSAI_ERR_SHAPE;
     if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return BONSAI_ERR_SHAPE;
@@ -218,6 +238,7 @@ const char *bonsai_status_string(int status) {
         case BONSAI_ERR_NOMEM: return "could not allocate the device workspace";
         case BONSAI_ERR_ALGO: return "the requested kernel cannot run this shape";
         case BONSAI_ERR_TOO_LARGE: return "the problem needs more than the fixed device scratch of the no-allocation entry point";
+        case BONSAI_ERR_ARG: return "unknown activation, layout, scaling or cache type, or a parameter outside its range";
         default: return "unknown status";
     }
 }
@@ -396,6 +417,163 @@ int bonsai_ternary_linear_swiglu(const uint16_t *x, const uint8_t *packed, const
     cudaError_t e = run_linear(chosen, x, packed, scales, y, M, N, K, fmt, 0, inner, s, st->info);
     if (e == cudaSuccess) e = launch_swiglu(y, h, M, F, s, st->info);
     return cuda_status(e);
+}
+
+int bonsai_ternary_linear_epilogue(const uint16_t *x, const uint8_t *packed, const uint16_t *scales,
+                                   const uint16_t *bias, const uint16_t *residual, uint16_t *y, int64_t M,
+                                   int64_t N, int64_t K, int fmt, int act, int algo, int split_k, void *stream) {
+    int rc = check_fmt(fmt);
+    if (rc != BONSAI_OK) return rc;
+    if (act < BONSAI_ACT_NONE || act > BONSAI_ACT_GELU_TANH) return BONSAI_ERR_ARG;
+    rc = check_shape(M, N, K);
+    if (rc != BONSAI_OK) return rc;
+    if (split_k < 0) return BONSAI_ERR_SHAPE;
+    if (M == 0 || N == 0) return BONSAI_OK;
+    if (!x || !packed || !scales || !y) return BONSAI_ERR_NULL;
+    if (!aligned16(x) || !aligned16(packed) || !aligned16(scales) || !aligned16(y) || !aligned16(bias) ||
+        !aligned16(residual))
+        return BONSAI_ERR_ALIGN;
+    int chosen = resolve_algo(algo, M, N, K, fmt);
+    if (chosen < 0) return chosen;
+    if (algo == BONSAI_ALGO_GEMM && split_k == 3) return BONSAI_ERR_ALGO;
+
+    std::lock_guard<std::mutex> lock(g_mutex);
+    int dev;
+    DeviceState *st;
+    rc = probe_current(&dev, &st);
+    if (rc != BONSAI_OK) return rc;
+    chosen = BONSAI_ALGO_SIMPLE;
+    Workspace ws;
+    rc = ensure_workspace(*st, workspace_for(chosen, M, N, K, fmt, split_k, st->info), 0, &ws);
+    if (rc != BONSAI_OK) return rc;
+    Epilogue epi;
+    epi.bias = bias;
+    epi.residual = residual;
+    epi.act = act;
+    return cuda_status(launch_linear_simple(x, packed, scales, y, M, N, K, fmt, ws, static_cast<cudaStream_t>(stream),
+                                            st->info, &epi));
+}
+
+int bonsai_rope_frequencies(double *freqs, double *magnitude, int64_t R, double base, int scaling, double factor,
+                            double original, double low, double high) {
+    if (R < 0 || R % 2 != 0 || R > kMaxRopeDim) return BONSAI_ERR_SHAPE;
+    if (scaling < BONSAI_ROPE_PLAIN || scaling > BONSAI_ROPE_BANDS) return BONSAI_ERR_ARG;
+    if (!(base > 1) || !std::isfinite(base)) return BONSAI_ERR_ARG;
+    if (scaling != BONSAI_ROPE_PLAIN && (!(factor >= 1) || !std::isfinite(factor))) return BONSAI_ERR_ARG;
+    const bool banded = scaling == BONSAI_ROPE_YARN || scaling == BONSAI_ROPE_BANDS;
+    if (banded && (!(original > 0) || !std::isfinite(original) || !(low > 0) || !(high > low) || !std::isfinite(high)))
+        return BONSAI_ERR_ARG;
+    if (!magnitude || (R > 0 && !freqs)) return BONSAI_ERR_NULL;
+    *magnitude = scaling == BONSAI_ROPE_YARN ? 1.0 + 0.1 * std::log(factor) : 1.0;
+    const double two_pi = 6.283185307179586476925;
+    // one pair alone has frequency 1 whatever the base
+    if (scaling == BONSAI_ROPE_NTK && R > 2) base *= std::pow(factor, (double)R / (double)(R - 2));
+    // YaRN: the pair indices that turn `high` and `low` times over `original` positions
+    double first = 0, last = 0;
+    if (scaling == BONSAI_ROPE_YARN) {
+        auto index_of = [&](double turns) { return R * std::log(original / (turns * two_pi)) / (2 * std::log(base)); };
+        first = std::floor(index_of(high));
+        last = std::ceil(index_of(low));
+        first = first < 0 ? 0 : first;
+        last = last > R - 1 ? R - 1 : last;
+    }
+    for (int64_t i = 0; i < R / 2; i++) {
+        const double f = std::pow(base, -2.0 * (double)i / (double)R);
+        double v = f;
+        if (scaling == BONSAI_ROPE_LINEAR) v = f / factor;
+        if (scaling == BONSAI_ROPE_YARN) {
+            const double width = last - first < 1e-3 ? 1e-3 : last - first;
+            double ramp = ((double)i - first) / width;
+            ramp = ramp < 0 ? 0 : ramp > 1 ? 1 : ramp;
+            v = f / factor * ramp + f * (1 - ramp);
+        }
+        if (scaling == BONSAI_ROPE_BANDS) {
+            double s = (original * f / two_pi - low) / (high - low);  // turns over `original` positions
+            s = s < 0 ? 0 : s > 1 ? 1 : s;
+            v = f / factor * (1 - s) + f * s;
+        }
+        freqs[i] = v;
+    }
+    return BONSAI_OK;
+}
+
+int bonsai_rope(const uint16_t *x, uint16_t *out, const double *freqs, const int32_t *positions, int64_t T, int64_t H,
+                int64_t D, int64_t R, int64_t ld_x, int64_t ld_out, float magnitude, int layout, void *stream) {
+    if (layout != BONSAI_ROPE_HALF && layout != BONSAI_ROPE_INTERLEAVED) return BONSAI_ERR_ARG;
+    if (T < 0 || T > kMaxDim || H < 0 || H > kMaxHeads || D <= 0 || D % 8 != 0 || D > kMaxRopeDim || R < 0 ||
+        R % 2 != 0 || R > D)
+        return BONSAI_ERR_SHAPE;
+    if (!row_stride_ok(ld_x, H * D) || !row_stride_ok(ld_out, H * D)) return BONSAI_ERR_SHAPE;
+    if (T == 0 || H == 0) return BONSAI_OK;
+    if (!x || !out || !positions || (R > 0 && !freqs)) return BONSAI_ERR_NULL;
+    if (!aligned16(x) || !aligned16(out) || !aligned_to(freqs, 8) || !aligned_to(positions, 4)) return BONSAI_ERR_ALIGN;
+    std::lock_guard<std::mutex> lock(g_mutex);
+    int dev;
+    DeviceState *st;
+    const int rc = probe_current(&dev, &st);
+    if (rc != BONSAI_OK) return rc;
+    const RopeArgs r = {freqs, positions, magnitude, (int)R, layout};
+    return cuda_status(launch_rope(x, out, r, T, H, D, ld_x, ld_out, static_cast<cudaStream_t>(stream), st->info));
+}
+
+int bonsai_rope_append(const uint16_t *qkv, uint16_t *q_out, void *k_cache, void *v_cache, const float *k_scale,
+                       const float *v_scale, const double *freqs, const int32_t *positions, const int64_t *slots,
+                       int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t R, int64_t ld_qkv, int64_t ld_q,
+                       int64_t pages, int64_t page_size, float magnitude, int layout, int kv_type, void *stream) {
+    if (layout != BONSAI_ROPE_HALF && layout != BONSAI_ROPE_INTERLEAVED) return BONSAI_ERR_ARG;
+    int rc = check_cache(Hq, Hkv, D, pages, page_size, kv_type);
+    if (rc != BONSAI_OK) return rc;
+    if (T < 0 || T > kMaxDim || R < 0 || R % 2 != 0 || R > D) return BONSAI_ERR_SHAPE;
+    if (!row_stride_ok(ld_qkv, (Hq + 2 * Hkv) * D) || !row_stride_ok(ld_q, Hq * D)) return BONSAI_ERR_SHAPE;
+    if (T == 0) return BONSAI_OK;
+    if (!qkv || (Hq > 0 && !q_out) || !k_cache || !v_cache || !positions || !slots || (R > 0 && !freqs))
+        return BONSAI_ERR_NULL;
+    if (kv_type == BONSAI_KV_E4M3 && (!k_scale || !v_scale)) return BONSAI_ERR_NULL;
+    if (!aligned16(qkv) || !aligned16(q_out) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned_to(freqs, 8) ||
+        !aligned_to(positions, 4) || !aligned_to(slots, 8) || !aligned_to(k_scale, 4) || !aligned_to(v_scale, 4))
+        return BONSAI_ERR_ALIGN;
+    std::lock_guard<std::mutex> lock(g_mutex);
+    int dev;
+    DeviceState *st;
+    rc = probe_current(&dev, &st);
+    if (rc != BONSAI_OK) return rc;
+    Workspace ws;  // the status word
+    rc = ensure_workspace(*st, 0, 0, &ws);
+    if (rc != BONSAI_OK) return rc;
+    const RopeArgs r = {freqs, positions, magnitude, (int)R, layout};
+    const KvCache c = {k_cache, v_cache, k_scale, v_scale, pages, (int)page_size, (int)Hkv, (int)D, kv_type};
+    return cuda_status(launch_rope_append(qkv, q_out, c, r, slots, T, Hq, ld_qkv, ld_q, ws,
+                                          static_cast<cudaStream_t>(stream), st->info));
+}
+
+int bonsai_paged_attention(const uint16_t *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                           const float *v_scale, const int32_t *page_table, const int32_t *lengths, uint16_t *out,
+                           float *lse, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t ld_q, int64_t ld_out,
+                           int64_t pages, int64_t page_size, int64_t max_pages, int64_t window, float scale,
+                           int kv_type, void *stream) {
+    int rc = check_cache(Hq, Hkv, D, pages, page_size, kv_type);
+    if (rc != BONSAI_OK) return rc;
+    if (B < 0 || B > kMaxSequences || Hq < 1 || max_pages < 1 || max_pages > kMaxDim || window < 0)
+        return BONSAI_ERR_SHAPE;
+    if (!row_stride_ok(ld_q, Hq * D) || !row_stride_ok(ld_out, Hq * D)) return BONSAI_ERR_SHAPE;
+    if (B == 0) return BONSAI_OK;
+    if (!q || !k_cache || !v_cache || !page_table || !lengths || !out) return BONSAI_ERR_NULL;
+    if (kv_type == BONSAI_KV_E4M3 && (!k_scale || !v_scale)) return BONSAI_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned_to(page_table, 4) ||
+        !aligned_to(lengths, 4) || !aligned_to(lse, 4) || !aligned_to(k_scale, 4) || !aligned_to(v_scale, 4))
+        return BONSAI_ERR_ALIGN;
+    std::lock_guard<std::mutex> lock(g_mutex);
+    int dev;
+    DeviceState *st;
+    rc = probe_current(&dev, &st);
+    if (rc != BONSAI_OK) return rc;
+    Workspace ws;
+    rc = ensure_workspace(*st, attention_workspace_bytes(B, Hq, Hkv, D, st->info), 0, &ws);
+    if (rc != BONSAI_OK) return rc;
+    const KvCache c = {const_cast<void *>(k_cache), const_cast<void *>(v_cache), k_scale, v_scale, pages,
+                       (int)page_size, (int)Hkv, (int)D, kv_type};
+    return cuda_status(launch_paged_attention(q, c, page_table, lengths, out, lse, B, Hq, ld_q, ld_out, max_pages,
+                                              window, scale, ws, static_cast<cudaStream_t>(stream), st->info));
 }
 
 int bonsai_launch_count(int64_t M, int64_t N, int64_t K, int fmt, int algo, int split_k) {

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "epilogue.cuh"
+
 namespace bonsai {
 
 struct DeviceInfo {
@@ -56,7 +58,8 @@ cudaError_t launch_hadamard_f32(const uint16_t *x, float *out, int64_t M, int64_
 size_t simple_workspace_bytes(int64_t M, int64_t N, int64_t K);
 cudaError_t launch_linear_simple(const uint16_t *x, const uint8_t *packed, const uint16_t *scales,
                                  uint16_t *y, int64_t M, int64_t N, int64_t K, int fmt,
-                                 const Workspace &ws, cudaStream_t s, const DeviceInfo &dev);
+                                 const Workspace &ws, cudaStream_t s, const DeviceInfo &dev,
+                                 const Epilogue *epi = nullptr);
 
 // ---- gemv_lut.cu: M == 1
 bool gemv_supported(int64_t M, int64_t N, int64_t K, int fmt);
@@ -86,6 +89,7 @@ constexpr size_t kCtlRegionBytes = 4096;
 constexpr unsigned int kDevStatusGemvCopyTimeout = 1u;   // integer GEMV: a weight copy never landed
 constexpr unsigned int kDevStatusGemvPieceTimeout = 2u;  // integer GEMV: a split tile's later piece never came
 constexpr unsigned int kDevStatusGemmTimeout = 4u;       // prefill GEMM: a barrier or hand-over wait gave up
+constexpr unsigned int kDevStatusCacheRange = 16u;       // append or attention: a slot, page or length outside the cache
 constexpr unsigned int kDevStatusSkinnyTimeout = 8u;     // skinny kernel: the wait for the rotated x, or a TMA copy, gave up
 
 // ---- gemv_imma.cu: M <= 3 (g64: 2), PQ2_0 and g64, integer tensor cores
@@ -122,5 +126,32 @@ size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, const Devi
 cudaError_t launch_gemm(const uint16_t *x, const uint8_t *packed, const uint16_t *scales,
                         uint16_t *y, int64_t M, int64_t N, int64_t K, int fmt, int tile_hint,
                         const Workspace &ws, cudaStream_t s, const DeviceInfo &dev, int64_t swiglu_f = 0);
+
+// ---- rope.cu: rotary positions, and their append to a paged cache
+struct RopeArgs {
+    const double *freqs;  // R / 2, radians per position
+    const int32_t *positions;
+    float magnitude;
+    int R, layout;  // rotated elements of a head; bonsai_rope_layout
+};
+// pools of pages x kv_heads x page_size x head_dim elements of bonsai_kv_type `type`
+struct KvCache {
+    void *k, *v;
+    const float *k_scale, *v_scale;  // E4M3: one per head
+    int64_t pages;
+    int page_size, kv_heads, head_dim, type;
+};
+cudaError_t launch_rope(const uint16_t *x, uint16_t *out, const RopeArgs &r, int64_t T, int64_t H, int64_t D,
+                        int64_t ld_x, int64_t ld_out, cudaStream_t s, const DeviceInfo &dev);
+cudaError_t launch_rope_append(const uint16_t *qkv, uint16_t *q_out, const KvCache &c, const RopeArgs &r,
+                               const int64_t *slots, int64_t T, int64_t Hq, int64_t ld_qkv, int64_t ld_q,
+                               const Workspace &ws, cudaStream_t s, const DeviceInfo &dev);
+
+// ---- attention.cu: one new token per sequence over a paged cache (table: B x width pages)
+size_t attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, const DeviceInfo &dev);
+cudaError_t launch_paged_attention(const uint16_t *q, const KvCache &c, const int32_t *table, const int32_t *lengths,
+                                   uint16_t *out, float *lse, int64_t B, int64_t Hq, int64_t ld_q, int64_t ld_out,
+                                   int64_t width, int64_t window, float scale, const Workspace &ws, cudaStream_t s,
+                                   const DeviceInfo &dev);
 
 }  // namespace bonsai

@@ -21,7 +21,7 @@ template <int kFmt>
 __global__ void __launch_bounds__(256) linear_simple_kernel(
     const float *__restrict__ xr, const uint8_t *__restrict__ packed,
     const uint16_t *__restrict__ scales, uint16_t *__restrict__ y, int64_t M, int64_t N,
-    int64_t K) {
+    int64_t K, Epilogue epi) {
     const int lane = threadIdx.x & 31;
     const int64_t G = K / kGroup;
     const int64_t mchunks = (M + kTokensPerWarp - 1) / kTokensPerWarp;
@@ -68,7 +68,8 @@ __global__ void __launch_bounds__(256) linear_simple_kernel(
         }
         for (int i = 0; i < kTokensPerWarp; i++) {
             const float total = warp_sum(acc[i]);
-            if (lane == 0 && m0 + i < M) y[(m0 + i) * N + n] = float_to_half_bits(total);
+            if (lane == 0 && m0 + i < M)
+                y[(m0 + i) * N + n] = float_to_half_bits(epilogue_value(total, epi, m0 + i, n, N));
         }
     }
 }
@@ -82,7 +83,8 @@ size_t simple_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 
 cudaError_t launch_linear_simple(const uint16_t *x, const uint8_t *packed, const uint16_t *scales,
                                  uint16_t *y, int64_t M, int64_t N, int64_t K, int fmt,
-                                 const Workspace &ws, cudaStream_t s, const DeviceInfo &dev) {
+                                 const Workspace &ws, cudaStream_t s, const DeviceInfo &dev, const Epilogue *epi) {
+    const Epilogue e = epi ? *epi : Epilogue{};
     float *xr = reinterpret_cast<float *>(ws.data);
     cudaError_t err = launch_hadamard_f32(x, xr, M, K, s, dev);
     if (err != cudaSuccess) return err;
@@ -91,13 +93,13 @@ cudaError_t launch_linear_simple(const uint16_t *x, const uint8_t *packed, const
     const int64_t cap = (int64_t)dev.sm_count * 16;
     const int grid = (int)(want < cap ? want : cap);
     if (fmt == 1)
-        linear_simple_kernel<1><<<grid, 256, 0, s>>>(xr, packed, scales, y, M, N, K);
+        linear_simple_kernel<1><<<grid, 256, 0, s>>>(xr, packed, scales, y, M, N, K, e);
     else if (fmt == 3)
-        linear_simple_kernel<3><<<grid, 256, 0, s>>>(xr, packed, scales, y, M, N, K);
+        linear_simple_kernel<3><<<grid, 256, 0, s>>>(xr, packed, scales, y, M, N, K, e);
     else if (fmt == 4)
-        linear_simple_kernel<4><<<grid, 256, 0, s>>>(xr, packed, scales, y, M, N, K);
+        linear_simple_kernel<4><<<grid, 256, 0, s>>>(xr, packed, scales, y, M, N, K, e);
     else
-        linear_simple_kernel<2><<<grid, 256, 0, s>>>(xr, packed, scales, y, M, N, K);
+        linear_simple_kernel<2><<<grid, 256, 0, s>>>(xr, packed, scales, y, M, N, K, e);
     return cudaGetLastError();
 }
 
