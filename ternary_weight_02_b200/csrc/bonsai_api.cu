@@ -186,13 +186,13 @@ int resolve_algo(int algo, int64_t M, int64_t N, int64_t K, int fmt, const Devic
 // Launches the chosen kernel (argument checks and the workspace are the caller's).
 cudaError_t run_linear(int chosen, const uint16_t *x, const uint8_t *packed, const uint16_t *scales, uint16_t *y,
                        int64_t M, int64_t N, int64_t K, int fmt, int split_k, const Workspace &ws, cudaStream_t s,
-                       const DeviceInfo &info) {
+                       const DeviceInfo &info, const Epilogue *epi = nullptr) {
     switch (chosen) {
-        case BONSAI_ALGO_GEMV: return launch_gemv(x, packed, scales, y, N, K, fmt, split_k, ws, s, info);
-        case BONSAI_ALGO_SKINNY: return launch_skinny(x, packed, scales, y, M, N, K, fmt, split_k, ws, s, info);
-        case BONSAI_ALGO_GEMM: return launch_gemm(x, packed, scales, y, M, N, K, fmt, split_k, ws, s, info);
-        case BONSAI_ALGO_IMMA: return launch_gemv_imma(x, packed, scales, y, M, N, K, fmt, ws, s, info);
-        default: return launch_linear_simple(x, packed, scales, y, M, N, K, fmt, ws, s, info);
+        case BONSAI_ALGO_GEMV: return launch_gemv(x, packed, scales, y, N, K, fmt, split_k, ws, s, info, epi);
+        case BONSAI_ALGO_SKINNY: return launch_skinny(x, packed, scales, y, M, N, K, fmt, split_k, ws, s, info, epi);
+        case BONSAI_ALGO_GEMM: return launch_gemm(x, packed, scales, y, M, N, K, fmt, split_k, ws, s, info, 0, epi);
+        case BONSAI_ALGO_IMMA: return launch_gemv_imma(x, packed, scales, y, M, N, K, fmt, ws, s, info, 0, epi);
+        default: return launch_linear_simple(x, packed, scales, y, M, N, K, fmt, ws, s, info, epi);
     }
 }
 
@@ -442,16 +442,20 @@ int bonsai_ternary_linear_epilogue(const uint16_t *x, const uint8_t *packed, con
     DeviceState *st;
     rc = probe_current(&dev, &st);
     if (rc != BONSAI_OK) return rc;
-    chosen = BONSAI_ALGO_SIMPLE;
+    if (algo == BONSAI_ALGO_AUTO) chosen = resolve_algo(algo, M, N, K, fmt, &st->info);
+    if (chosen == BONSAI_ALGO_IMMA && !gemv_imma_grid_fits(N, K, st->info)) return BONSAI_ERR_ALGO;
     Workspace ws;
-    rc = ensure_workspace(*st, workspace_for(chosen, M, N, K, fmt, split_k, st->info), 0, &ws);
+    rc = ensure_workspace(*st, workspace_for(chosen, M, N, K, fmt, split_k, st->info),
+                          chosen == BONSAI_ALGO_IMMA ? gemv_imma_zeroed_bytes(M, N, K) : 0, &ws);
     if (rc != BONSAI_OK) return rc;
     Epilogue epi;
     epi.bias = bias;
     epi.residual = residual;
     epi.act = act;
-    return cuda_status(launch_linear_simple(x, packed, scales, y, M, N, K, fmt, ws, static_cast<cudaStream_t>(stream),
-                                            st->info, &epi));
+    // without any of the three the call is the plain product
+    const Epilogue *e = bias || residual || act != BONSAI_ACT_NONE ? &epi : nullptr;
+    return cuda_status(run_linear(chosen, x, packed, scales, y, M, N, K, fmt, split_k, ws,
+                                  static_cast<cudaStream_t>(stream), st->info, e));
 }
 
 int bonsai_rope_frequencies(double *freqs, double *magnitude, int64_t R, double base, int scaling, double factor,

@@ -328,6 +328,37 @@ __device__ __forceinline__ unsigned int ld_acquire_u32(const unsigned int *p) {
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
+// Bias, activation and residual on 32 consecutive columns n0 .. n0 + 31 of row m (FP32 bits in v).
+// Columns past N and rows past M belong to no output and are left as they are.
+__device__ __forceinline__ void epilogue_row32(uint32_t *v, const Epilogue &e, int64_t m, int64_t M, int64_t n0,
+                                               int64_t N) {
+    if (m >= M || n0 >= N) return;
+    if (n0 + 32 <= N && (N & 7) == 0) {
+        uint4 b[4], r[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            if (e.bias) b[j] = __ldcg(reinterpret_cast<const uint4 *>(e.bias + n0) + j);
+            if (e.residual) r[j] = __ldcg(reinterpret_cast<const uint4 *>(e.residual + m * N + n0) + j);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const uint32_t bw[4] = {b[j].x, b[j].y, b[j].z, b[j].w}, rw[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                float z = __uint_as_float(v[8 * j + k]);
+                if (e.bias) z += half_bits_to_float((uint16_t)(bw[k >> 1] >> (16 * (k & 1))));
+                z = activate(z, e.act);
+                if (e.residual) z += half_bits_to_float((uint16_t)(rw[k >> 1] >> (16 * (k & 1))));
+                v[8 * j + k] = __float_as_uint(z);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 32; k++)
+        if (n0 + k < N) v[k] = __float_as_uint(epilogue_value(__uint_as_float(v[k]), e, m, n0 + k, N));
+}
+
 // The eight expansion/epilogue warps (256 threads) meet here; barrier 0 is __syncthreads.
 __device__ __forceinline__ void expand_warps_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
@@ -374,13 +405,16 @@ __device__ __forceinline__ void expand_warps_sync() { asm volatile("bar.sync 1, 
 // slots and flags stay per CTA, work is split per pair.  Only an explicit request takes
 // this mode: on the 27B-class projections it runs a few per cent behind single-CTA
 // tiles, whose x' traffic per MMA it shares, so halving the expansion buys nothing there.
-template <int kFmt, int kAcc, bool kSwiglu, bool kPair>
+// kEpi: bias, activation and residual of `epi` on the FP32 sums, in registers before the one
+// rounding to FP16 (never with kSwiglu or kPair).  A thread holds 32 consecutive columns of one
+// row there: it reads their residual as four 16-byte loads where rows are 16-byte aligned.
+template <int kFmt, int kAcc, bool kSwiglu, bool kPair, bool kEpi = false>
 __global__ void __launch_bounds__(kThreads, 1) gemm_tcgen05_kernel(
     const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap w_map,
     const uint8_t *__restrict__ packed,
     const uint16_t *__restrict__ scales, uint16_t *__restrict__ y, float *__restrict__ partials,
     const uint16_t *__restrict__ x, uint16_t *__restrict__ xr, int64_t nblocks, unsigned int *__restrict__ ctl,
-    uint32_t wait_limit, uint32_t epoch_skew, int M, int N, int K, int mt, int F) {
+    uint32_t wait_limit, uint32_t epoch_skew, int M, int N, int K, int mt, int F, Epilogue epi) {
     using C = Cfg<kAcc, kPair>;
     constexpr int STAGES = C::kStages;
     constexpr int kSlotFloats = C::kTileM * BN;
@@ -972,6 +1006,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tcgen05_kernel(
 #pragma unroll
                                 for (int i = 0; i < 32; i++) vc[i] = 0x7fc00000u;
                         }
+                        if constexpr (kEpi)
+                            epilogue_row32(vc, epi, (int64_t)acc_row0(tm, a) + 32 * q + lane, M,
+                                           (int64_t)tn * BN + half * 128 + 32 * c, N);
                         // FP16 (nearest even) into the staging row of this lane
 #pragma unroll
                         for (int j = 0; j < 4; j++) {
@@ -1108,8 +1145,11 @@ size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, const Devi
 
 cudaError_t launch_gemm(const uint16_t *x, const uint8_t *packed, const uint16_t *scales,
                         uint16_t *y, int64_t M, int64_t N, int64_t K, int fmt, int tile_hint,
-                        const Workspace &ws, cudaStream_t s, const DeviceInfo &dev, int64_t swiglu_f) {
+                        const Workspace &ws, cudaStream_t s, const DeviceInfo &dev, int64_t swiglu_f,
+                        const Epilogue *epi) {
     const bool swiglu = swiglu_f > 0;
+    if (epi && (swiglu || tile_hint == 3)) return cudaErrorInvalidValue;
+    const Epilogue ep = epi ? *epi : Epilogue{};
     if (swiglu && N != 2 * swiglu_f) return cudaErrorInvalidValue;
     GemmPlan plan = gemm_plan(M, N, K, tile_hint, dev.sm_count);
     if (ws.data_bytes < gemm_workspace_bytes(M, N, K, fmt, dev) || plan.ctas > kCtlGemmMaxCtas ||
@@ -1150,7 +1190,7 @@ cudaError_t launch_gemm(const uint16_t *x, const uint8_t *packed, const uint16_t
         if (e != cudaSuccess) return e;
         if (!plan.pair) {
             kern<<<plan.ctas, kThreads, smem, s>>>(map, wmap, packed, scales, y, partials, x, xr, nblocks, ctl, limit,
-                                                   skew, (int)M, (int)N, (int)K, plan.mt, (int)swiglu_f);
+                                                   skew, (int)M, (int)N, (int)K, plan.mt, (int)swiglu_f, ep);
             return cudaGetLastError();
         }
         // clusters of two; only as many pairs as fit at once (the rotation phase's grid
@@ -1173,7 +1213,7 @@ cudaError_t launch_gemm(const uint16_t *x, const uint8_t *packed, const uint16_t
         if (clusters < 1) return cudaErrorInvalidConfiguration;
         if (plan.ctas > 2 * clusters) cfg.gridDim = dim3((unsigned)(2 * clusters));
         return cudaLaunchKernelEx(&cfg, kern, map, wmap, packed, scales, y, partials, x, xr, nblocks, ctl, limit, skew,
-                                  (int)M, (int)N, (int)K, plan.mt, (int)swiglu_f);
+                                  (int)M, (int)N, (int)K, plan.mt, (int)swiglu_f, ep);
     };
     auto pick = [&](auto k1, auto k2) {
         if (plan.pair) return plan.acc == 2 ? go(k2, Cfg<2, true>::kSmemBytes) : go(k1, Cfg<1, true>::kSmemBytes);
@@ -1190,6 +1230,12 @@ cudaError_t launch_gemm(const uint16_t *x, const uint8_t *packed, const uint16_t
         if (fmt == 3) return pick(gemm_tcgen05_kernel<3, 1, false, true>, gemm_tcgen05_kernel<3, 2, false, true>);
         if (fmt == 4) return pick(gemm_tcgen05_kernel<4, 1, false, true>, gemm_tcgen05_kernel<4, 2, false, true>);
         return pick(gemm_tcgen05_kernel<2, 1, false, true>, gemm_tcgen05_kernel<2, 2, false, true>);
+    }
+    if (epi) {
+        if (fmt == 1) return pick(gemm_tcgen05_kernel<1, 1, false, false, true>, gemm_tcgen05_kernel<1, 2, false, false, true>);
+        if (fmt == 3) return pick(gemm_tcgen05_kernel<3, 1, false, false, true>, gemm_tcgen05_kernel<3, 2, false, false, true>);
+        if (fmt == 4) return pick(gemm_tcgen05_kernel<4, 1, false, false, true>, gemm_tcgen05_kernel<4, 2, false, false, true>);
+        return pick(gemm_tcgen05_kernel<2, 1, false, false, true>, gemm_tcgen05_kernel<2, 2, false, false, true>);
     }
     if (swiglu) {
         if (fmt == 1) return pick(gemm_tcgen05_kernel<1, 1, true, false>, gemm_tcgen05_kernel<1, 2, true, false>);

@@ -64,6 +64,8 @@
 //   CTA exits, waits (again bounded) for the copies it had started; an owner whose wait
 //   for a later piece gives up writes NaN for that tile.  Both set a bit in the
 //   workspace's device status word.
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 #include "tma.cuh"
@@ -295,11 +297,12 @@ __device__ __forceinline__ float wait_pairs(const uint64_t *p, int lane, uint32_
 // hook that makes those waits give up.
 //
 // kM: tokens (1 to 3; g64 1 or 2); x is kM x K and y kM x N (kSwiglu: kM x F), row-major.
-template <bool kAsyncScales, bool kSwiglu, bool kG64, int kM>
+// kEpi: bias, activation and residual of `epi` on the sums (never with kSwiglu).
+template <bool kAsyncScales, bool kSwiglu, bool kG64, int kM, bool kEpi = false>
 __global__ void __launch_bounds__(kThreads, 1) gemv_imma_kernel(
     const __grid_constant__ CUtensorMap wmap, const uint16_t *__restrict__ x, const uint16_t *__restrict__ scales,
     uint16_t *__restrict__ y, uint64_t *__restrict__ partials, unsigned int *__restrict__ ctl, int N, int K, int F,
-    uint32_t wait_limit, uint32_t epoch_skew) {
+    uint32_t wait_limit, uint32_t epoch_skew, Epilogue epi) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -486,7 +489,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_imma_kernel(
                 continue;
             }
             const int row = rt * kItemRows + lane;
-            if (row < N) y[(int64_t)m * N + row] = float_to_half_bits(sum);
+            if (row < N) {
+                if (kEpi) sum = epilogue_value(sum, epi, m, row, N);
+                y[(int64_t)m * N + row] = float_to_half_bits(sum);
+            }
         }
     };
 
@@ -808,7 +814,8 @@ size_t gemv_imma_zeroed_bytes(int64_t M, int64_t N, int64_t K) {
 
 cudaError_t launch_gemv_imma(const uint16_t *x, const uint8_t *packed, const uint16_t *scales, uint16_t *y,
                              int64_t M, int64_t N, int64_t K, int fmt, const Workspace &ws, cudaStream_t s,
-                             const DeviceInfo &dev, int64_t swiglu_f) {
+                             const DeviceInfo &dev, int64_t swiglu_f, const Epilogue *epi) {
+    if (swiglu_f > 0 && epi) return cudaErrorInvalidValue;
     if ((fmt != 2 && fmt != 4) || !gemv_imma_supported(M, N, K, fmt)) return cudaErrorInvalidValue;
     const bool swiglu = swiglu_f > 0;
     if (swiglu && N != 2 * swiglu_f) return cudaErrorInvalidValue;
@@ -838,24 +845,25 @@ cudaError_t launch_gemv_imma(const uint16_t *x, const uint8_t *packed, const uin
     // with the item
     using Kern = decltype(&gemv_imma_kernel<true, true, true, 1>);
     const bool async = K % kItemK == 0;
+    // the kernel of (scale copies, SwiGLU or epilogue) for the packing and the tokens
+    auto pick = [&](auto g64, auto tokens) -> Kern {
+        constexpr bool kG64 = decltype(g64)::value;
+        constexpr int kM = decltype(tokens)::value;
+        if (epi) return async ? gemv_imma_kernel<true, false, kG64, kM, true> : gemv_imma_kernel<false, false, kG64, kM, true>;
+        if (swiglu) return async ? gemv_imma_kernel<true, true, kG64, kM> : gemv_imma_kernel<false, true, kG64, kM>;
+        return async ? gemv_imma_kernel<true, false, kG64, kM> : gemv_imma_kernel<false, false, kG64, kM>;
+    };
+    using std::false_type, std::true_type;
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    using Three = std::integral_constant<int, 3>;
     Kern kern;
-    if (M == 3) {
-        kern = async ? (swiglu ? gemv_imma_kernel<true, true, false, 3> : gemv_imma_kernel<true, false, false, 3>)
-                     : (swiglu ? gemv_imma_kernel<false, true, false, 3> : gemv_imma_kernel<false, false, false, 3>);
-    } else if (M == 2) {
-        if (fmt == 4)
-            kern = async ? (swiglu ? gemv_imma_kernel<true, true, true, 2> : gemv_imma_kernel<true, false, true, 2>)
-                         : (swiglu ? gemv_imma_kernel<false, true, true, 2> : gemv_imma_kernel<false, false, true, 2>);
-        else
-            kern = async ? (swiglu ? gemv_imma_kernel<true, true, false, 2> : gemv_imma_kernel<true, false, false, 2>)
-                         : (swiglu ? gemv_imma_kernel<false, true, false, 2> : gemv_imma_kernel<false, false, false, 2>);
-    } else if (fmt == 4) {
-        kern = async ? (swiglu ? gemv_imma_kernel<true, true, true, 1> : gemv_imma_kernel<true, false, true, 1>)
-                     : (swiglu ? gemv_imma_kernel<false, true, true, 1> : gemv_imma_kernel<false, false, true, 1>);
-    } else {
-        kern = async ? (swiglu ? gemv_imma_kernel<true, true, false, 1> : gemv_imma_kernel<true, false, false, 1>)
-                     : (swiglu ? gemv_imma_kernel<false, true, false, 1> : gemv_imma_kernel<false, false, false, 1>);
-    }
+    if (M == 3)
+        kern = pick(false_type{}, Three{});
+    else if (M == 2)
+        kern = fmt == 4 ? pick(true_type{}, Two{}) : pick(false_type{}, Two{});
+    else
+        kern = fmt == 4 ? pick(true_type{}, One{}) : pick(false_type{}, One{});
     // the attribute is set to the largest layout any K takes, so that launches of several
     // sizes captured into one graph all stay within it
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -874,7 +882,7 @@ cudaError_t launch_gemv_imma(const uint16_t *x, const uint8_t *packed, const uin
     const uint32_t limit = dev.force_wait_timeouts ? kForcedWaitPolls : kSpinLimit;
     const uint32_t skew = dev.force_wait_timeouts ? 0x80000000u : 0u;
     return cudaLaunchKernelEx(&cfg, kern, wmap, x, scales, y, partials, ctl, (int)N, (int)K, (int)swiglu_f, limit,
-                              skew);
+                              skew, epi ? *epi : Epilogue{});
 }
 
 }  // namespace bonsai

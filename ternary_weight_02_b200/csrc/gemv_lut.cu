@@ -349,11 +349,11 @@ __device__ __forceinline__ void make_pbase(uint32_t (&pbase)[4], int lane) {
 
 // ---------------------------------------------------------------- split mode
 
-template <int kFmt>
+template <int kFmt, bool kEpi>
 __global__ void __launch_bounds__(kThreads, 1) gemv_split_kernel(
     const uint16_t *__restrict__ x, const uint8_t *__restrict__ packed,
     const uint16_t *__restrict__ scales, uint16_t *__restrict__ y, float *__restrict__ partials, int64_t N,
-    int64_t K, int parts) {
+    int64_t K, int parts, Epilogue epi) {
     extern __shared__ __align__(16) uint8_t smem[];
     float *xr = reinterpret_cast<float *>(smem);
     const uint32_t smem_addr = (uint32_t)__cvta_generic_to_shared(smem);
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_split_kernel(
         const int row = lane & 15;
         if (lane < 16 && n0 + row < N) {
             if (S == 1)
-                y[n0 + row] = float_to_half_bits(total);
+                y[n0 + row] = float_to_half_bits(kEpi ? epilogue_value(total, epi, 0, n0 + row, N) : total);
             else
                 partials[(int64_t)slice * N + n0 + row] = total;
         }
@@ -434,8 +434,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_split_kernel(
 
 // y[n] = sum over slices s (in order) of partials[s][n]; launched right after the split
 // kernel, it waits for that kernel to finish before reading.
+template <bool kEpi>
 __global__ void __launch_bounds__(256) gemv_reduce_kernel(const float *__restrict__ partials,
-                                                          uint16_t *__restrict__ y, int64_t N, int S) {
+                                                          uint16_t *__restrict__ y, int64_t N, int S, Epilogue epi) {
     pdl_launch_dependents();
     pdl_wait();
     for (int64_t n = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; n < N; n += (int64_t)gridDim.x * blockDim.x) {
@@ -449,6 +450,7 @@ __global__ void __launch_bounds__(256) gemv_reduce_kernel(const float *__restric
             for (int u = 0; u < 8; u++) acc += t[u];
         }
         for (; s < S; s++) acc += __ldcg(partials + (int64_t)s * N + n);
+        if (kEpi) acc = epilogue_value(acc, epi, 0, n, N);
         y[n] = float_to_half_bits(acc);
     }
 }
@@ -458,10 +460,10 @@ __global__ void __launch_bounds__(256) gemv_reduce_kernel(const float *__restric
 // A CTA owns row blocks [rb_begin, rb_end); in rounds of kWarps blocks (one per warp)
 // it walks all K slices.  Each warp keeps the scaled group sums of its block in two
 // registers across slices and reduces over the groups once at the end.
-template <int kFmt>
+template <int kFmt, bool kEpi>
 __global__ void __launch_bounds__(kThreads, 1) gemv_rows_kernel(
     const uint16_t *__restrict__ x, const uint8_t *__restrict__ packed,
-    const uint16_t *__restrict__ scales, uint16_t *__restrict__ y, int64_t N, int64_t K) {
+    const uint16_t *__restrict__ scales, uint16_t *__restrict__ y, int64_t N, int64_t K, Epilogue epi) {
     extern __shared__ __align__(16) uint8_t smem[];
     float *xr = reinterpret_cast<float *>(smem);  // x' of all K (K <= kRowsModeMaxK)
     const uint32_t smem_addr = (uint32_t)__cvta_generic_to_shared(smem);
@@ -525,7 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_rows_kernel(
         const float total = groups_total(acc, lane);
         const int64_t n0 = rb * kRows;
         const int row = lane & 15;
-        if (active && lane < 16 && n0 + row < N) y[n0 + row] = float_to_half_bits(total);
+        if (active && lane < 16 && n0 + row < N)
+            y[n0 + row] = float_to_half_bits(kEpi ? epilogue_value(total, epi, 0, n0 + row, N) : total);
     }
 }
 
@@ -584,20 +587,32 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), int grid, cudaStream_t s, Args.
 }
 
 // Split mode: the slice kernel, then (K > 512) the in-order reduction of its partials.
+// The epilogue belongs to the kernel that writes y.
 cudaError_t launch_split(const uint16_t *x, const uint8_t *packed, const uint16_t *scales, uint16_t *y,
-                         float *partials, int64_t N, int64_t K, int fmt, cudaStream_t s, const DeviceInfo &dev) {
+                         float *partials, int64_t N, int64_t K, int fmt, cudaStream_t s, const DeviceInfo &dev,
+                         const Epilogue *epi) {
     const int parts = gemv_parts(N, K, fmt, dev);
     const int64_t S = K / slice_k(fmt);
     const int64_t grid = S * parts;
     if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-    cudaError_t e = fmt == 1   ? launch_pdl(gemv_split_kernel<1>, (int)grid, s, x, packed, scales, y, partials, N, K, parts)
-                    : fmt == 3 ? launch_pdl(gemv_split_kernel<3>, (int)grid, s, x, packed, scales, y, partials, N, K, parts)
-                    : fmt == 4 ? launch_pdl(gemv_split_kernel<4>, (int)grid, s, x, packed, scales, y, partials, N, K, parts)
-                               : launch_pdl(gemv_split_kernel<2>, (int)grid, s, x, packed, scales, y, partials, N, K, parts);
+    const Epilogue ep = epi ? *epi : Epilogue{};
+    auto go = [&](auto kern) { return launch_pdl(kern, (int)grid, s, x, packed, scales, y, partials, N, K, parts, ep); };
+    cudaError_t e;
+    if (epi && S == 1)
+        e = fmt == 1   ? go(gemv_split_kernel<1, true>)
+            : fmt == 3 ? go(gemv_split_kernel<3, true>)
+            : fmt == 4 ? go(gemv_split_kernel<4, true>)
+                       : go(gemv_split_kernel<2, true>);
+    else
+        e = fmt == 1   ? go(gemv_split_kernel<1, false>)
+            : fmt == 3 ? go(gemv_split_kernel<3, false>)
+            : fmt == 4 ? go(gemv_split_kernel<4, false>)
+                       : go(gemv_split_kernel<2, false>);
     if (e != cudaSuccess || S == 1) return e;
     const int64_t rgrid64 = (N + 255) / 256;
     const int rgrid = (int)(rgrid64 < 4 * (int64_t)dev.sm_count ? rgrid64 : 4 * (int64_t)dev.sm_count);
-    return launch_pdl_cfg(gemv_reduce_kernel, rgrid, 256, 0, s, (const float *)partials, y, N, (int)S);
+    return launch_pdl_cfg(epi ? gemv_reduce_kernel<true> : gemv_reduce_kernel<false>, rgrid, 256, 0, s,
+                          (const float *)partials, y, N, (int)S, ep);
 }
 
 }  // namespace
@@ -629,17 +644,19 @@ size_t gemv_workspace_bytes(int64_t N, int64_t K, int fmt, int split_k, const De
 
 cudaError_t launch_gemv(const uint16_t *x, const uint8_t *packed, const uint16_t *scales,
                         uint16_t *y, int64_t N, int64_t K, int fmt, int split_k,
-                        const Workspace &ws, cudaStream_t s, const DeviceInfo &dev) {
+                        const Workspace &ws, cudaStream_t s, const DeviceInfo &dev, const Epilogue *epi) {
     // the dynamic allocation must start below kTableAddr - kMiscBytes in the shared
     // window; it starts right after the per-block reserved area (no static shared memory)
     if (dev.smem_reserved + kMiscBytes > (int)kTableAddr) return cudaErrorNotSupported;
     if (pick_rows_mode(N, K, fmt, split_k, dev)) {
         const int64_t RB = (N + kRows - 1) / kRows;
         const int grid = (int)(RB < dev.sm_count ? RB : dev.sm_count);
-        if (fmt == 1) return launch_pdl(gemv_rows_kernel<1>, grid, s, x, packed, scales, y, N, K);
-        return launch_pdl(gemv_rows_kernel<2>, grid, s, x, packed, scales, y, N, K);
+        const Epilogue ep = epi ? *epi : Epilogue{};
+        auto go = [&](auto kern) { return launch_pdl(kern, grid, s, x, packed, scales, y, N, K, ep); };
+        if (epi) return fmt == 1 ? go(gemv_rows_kernel<1, true>) : go(gemv_rows_kernel<2, true>);
+        return fmt == 1 ? go(gemv_rows_kernel<1, false>) : go(gemv_rows_kernel<2, false>);
     }
-    return launch_split(x, packed, scales, y, reinterpret_cast<float *>(ws.data), N, K, fmt, s, dev);
+    return launch_split(x, packed, scales, y, reinterpret_cast<float *>(ws.data), N, K, fmt, s, dev, epi);
 }
 
 // Split-mode launch with caller-provided scratch for the FP32 partials, whatever the shape;
@@ -655,7 +672,7 @@ cudaError_t launch_gemv_split_scratch(const uint16_t *x, const uint8_t *packed, 
                                       size_t partial_floats, cudaStream_t s, const DeviceInfo &dev) {
     if (gemv_split_partial_floats(N, K) > partial_floats) return cudaErrorInvalidValue;
     if (dev.smem_reserved + kMiscBytes > (int)kTableAddr) return cudaErrorNotSupported;
-    return launch_split(x, packed, scales, y, partials, N, K, fmt, s, dev);
+    return launch_split(x, packed, scales, y, partials, N, K, fmt, s, dev, nullptr);
 }
 
 }  // namespace bonsai

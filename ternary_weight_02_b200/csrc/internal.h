@@ -67,7 +67,7 @@ size_t gemv_workspace_bytes(int64_t N, int64_t K, int fmt, int split_k, const De
 int gemv_launches(int64_t N, int64_t K, int fmt, int split_k, const DeviceInfo &dev);
 cudaError_t launch_gemv(const uint16_t *x, const uint8_t *packed, const uint16_t *scales,
                         uint16_t *y, int64_t N, int64_t K, int fmt, int split_k,
-                        const Workspace &ws, cudaStream_t s, const DeviceInfo &dev);
+                        const Workspace &ws, cudaStream_t s, const DeviceInfo &dev, const Epilogue *epi = nullptr);
 
 // split-mode GEMV on caller-provided scratch for its FP32 partials (no-allocation entry point)
 size_t gemv_split_partial_floats(int64_t N, int64_t K);
@@ -96,10 +96,10 @@ constexpr unsigned int kDevStatusSkinnyTimeout = 8u;     // skinny kernel: the w
 bool gemv_imma_supported(int64_t M, int64_t N, int64_t K, int fmt);
 size_t gemv_imma_zeroed_bytes(int64_t M, int64_t N, int64_t K);  // of Workspace::zeroed
 bool gemv_imma_grid_fits(int64_t N, int64_t K, const DeviceInfo &dev);
-// swiglu_f > 0: fused gate/up rows, write silu(gate) * up (M x swiglu_f).
+// swiglu_f > 0: fused gate/up rows, write silu(gate) * up (M x swiglu_f); epi: not with swiglu_f.
 cudaError_t launch_gemv_imma(const uint16_t *x, const uint8_t *packed, const uint16_t *scales, uint16_t *y,
                              int64_t M, int64_t N, int64_t K, int fmt, const Workspace &ws, cudaStream_t s,
-                             const DeviceInfo &dev, int64_t swiglu_f = 0);
+                             const DeviceInfo &dev, int64_t swiglu_f = 0, const Epilogue *epi = nullptr);
 
 // ---- skinny_mma.cu: 1 <= M <= 16 (one launch when its grid is resident at once: the
 // rotation, a barrier on the call counter in Workspace::zeroed, the kernel; else two)
@@ -109,7 +109,7 @@ size_t skinny_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, int spli
 int skinny_launches(int64_t M, int64_t N, int64_t K, int fmt, int split_k, const DeviceInfo &dev);
 cudaError_t launch_skinny(const uint16_t *x, const uint8_t *packed, const uint16_t *scales,
                           uint16_t *y, int64_t M, int64_t N, int64_t K, int fmt, int split_k,
-                          const Workspace &ws, cudaStream_t s, const DeviceInfo &dev);
+                          const Workspace &ws, cudaStream_t s, const DeviceInfo &dev, const Epilogue *epi = nullptr);
 
 // ---- swiglu.cu: h = silu(y[:, :F]) * y[:, F:] for an M x 2F FP16 y
 cudaError_t launch_swiglu(const uint16_t *y, uint16_t *h, int64_t M, int64_t F, cudaStream_t s,
@@ -125,7 +125,8 @@ size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, const Devi
 // gets silu(gate) * up, M x swiglu_f.
 cudaError_t launch_gemm(const uint16_t *x, const uint8_t *packed, const uint16_t *scales,
                         uint16_t *y, int64_t M, int64_t N, int64_t K, int fmt, int tile_hint,
-                        const Workspace &ws, cudaStream_t s, const DeviceInfo &dev, int64_t swiglu_f = 0);
+                        const Workspace &ws, cudaStream_t s, const DeviceInfo &dev, int64_t swiglu_f = 0,
+                        const Epilogue *epi = nullptr);
 
 // ---- rope.cu: rotary positions, and their append to a paged cache
 struct RopeArgs {

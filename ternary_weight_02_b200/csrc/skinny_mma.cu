@@ -207,13 +207,13 @@ __global__ void __launch_bounds__(256) skinny_prep_kernel(const uint16_t *__rest
 // per stage, instead of the register ring: the copies in flight then do not hold
 // registers or load slots.  wmap and smap are the packed plane's and the scale plane's
 // tensor maps (unused otherwise).  Needs K a multiple of 1024 and chunks of whole stages.
-template <int NT, int kFmt, bool kTma>  // n8 token tiles: 1 (M <= 8) or 2 (M <= 16)
+template <int NT, int kFmt, bool kTma, bool kEpi>  // n8 token tiles: 1 (M <= 8) or 2 (M <= 16)
 __global__ void __launch_bounds__(kThreads) skinny_kernel(
     uint16_t *__restrict__ xsg, float *__restrict__ gsg, const uint8_t *__restrict__ packed,
     const uint16_t *__restrict__ scales, uint16_t *__restrict__ y, float *__restrict__ partials,
     unsigned int *__restrict__ counters, int M, int64_t N, int64_t K, int S, int gpc,
     const uint16_t *__restrict__ x, unsigned int *__restrict__ ctl, const __grid_constant__ CUtensorMap wmap,
-    const __grid_constant__ CUtensorMap smap) {
+    const __grid_constant__ CUtensorMap smap, Epilogue epi) {
     constexpr int MT = NT * 8;  // tokens padded
     static_assert(sub_groups<NT>() % kRing == 0, "ring slots follow the group index");
     static_assert(!kTma || (kFmt != 1 && sub_groups_tma<NT>() % kTGroups == 0), "TMA stages follow the group index");
@@ -556,7 +556,10 @@ __global__ void __launch_bounds__(kThreads) skinny_kernel(
             for (int e = 0; e < 4; e++) {
                 const int m = nt * 8 + 2 * tq + (e & 1);
                 const int64_t r = e < 2 ? r0 : r1;
-                if (m < M && r < N) y[(int64_t)m * N + r] = float_to_half_bits(acc[nt][e]);
+                if (m < M && r < N) {
+                    const float v = kEpi ? epilogue_value(acc[nt][e], epi, m, r, N) : acc[nt][e];
+                    y[(int64_t)m * N + r] = float_to_half_bits(v);
+                }
             }
         return;
     }
@@ -583,6 +586,7 @@ __global__ void __launch_bounds__(kThreads) skinny_kernel(
         if (r >= N) continue;
         float a = 0.f;
         for (int c = 0; c < S; c++) a += __ldcg(partials + ((int64_t)c * M + m) * N + r);
+        if (kEpi) a = epilogue_value(a, epi, m, r, N);
         y[(int64_t)m * N + r] = float_to_half_bits(a);
     }
     if (lane == 0) counters[rb] = 0u;
@@ -631,9 +635,9 @@ size_t gsum_bytes(int64_t M, int64_t K) {  // room for the g64 half sums
 
 // The kernel instance for (M, fmt, ring), its shared memory, and whether its grid is
 // resident on the GPU at once (then the rotation runs inside it: one launch).
-template <int NT, int kFmt, bool kTma>
+template <int NT, int kFmt, bool kTma, bool kEpi>
 cudaError_t kernel_fits(int64_t grid_ctas, int smem, const DeviceInfo &dev, bool *fits) {
-    auto kern = skinny_kernel<NT, kFmt, kTma>;
+    auto kern = skinny_kernel<NT, kFmt, kTma, kEpi>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     int per_sm = 0;
@@ -643,18 +647,19 @@ cudaError_t kernel_fits(int64_t grid_ctas, int smem, const DeviceInfo &dev, bool
     return cudaSuccess;
 }
 
-template <int NT>
+template <int NT, bool kEpi>
 cudaError_t kernel_fits_fmt(int fmt, bool tma, int64_t ctas, int smem, const DeviceInfo &dev, bool *fits) {
     if (tma)
-        return fmt == 4   ? kernel_fits<NT, 4, true>(ctas, smem, dev, fits)
-               : fmt == 3 ? kernel_fits<NT, 3, true>(ctas, smem, dev, fits)
-                          : kernel_fits<NT, 2, true>(ctas, smem, dev, fits);
-    return fmt == 4   ? kernel_fits<NT, 4, false>(ctas, smem, dev, fits)
-           : fmt == 3 ? kernel_fits<NT, 3, false>(ctas, smem, dev, fits)
-           : fmt == 1 ? kernel_fits<NT, 1, false>(ctas, smem, dev, fits)
-                      : kernel_fits<NT, 2, false>(ctas, smem, dev, fits);
+        return fmt == 4   ? kernel_fits<NT, 4, true, kEpi>(ctas, smem, dev, fits)
+               : fmt == 3 ? kernel_fits<NT, 3, true, kEpi>(ctas, smem, dev, fits)
+                          : kernel_fits<NT, 2, true, kEpi>(ctas, smem, dev, fits);
+    return fmt == 4   ? kernel_fits<NT, 4, false, kEpi>(ctas, smem, dev, fits)
+           : fmt == 3 ? kernel_fits<NT, 3, false, kEpi>(ctas, smem, dev, fits)
+           : fmt == 1 ? kernel_fits<NT, 1, false, kEpi>(ctas, smem, dev, fits)
+                      : kernel_fits<NT, 2, false, kEpi>(ctas, smem, dev, fits);
 }
 
+template <bool kEpi>
 cudaError_t grid_fits(int64_t M, int64_t N, int64_t K, int fmt, int split_k, const DeviceInfo &dev, bool *fits) {
     const bool tma = use_tma(K, fmt);
     int S, gpc;
@@ -662,8 +667,8 @@ cudaError_t grid_fits(int64_t M, int64_t N, int64_t K, int fmt, int split_k, con
     const int64_t ctas = ((N + kRowsPerCta - 1) / kRowsPerCta) * S;
     const int NT = M <= 8 ? 1 : 2;
     const int smem = smem_bytes(NT, gpc, fmt, tma);
-    return NT == 1 ? kernel_fits_fmt<1>(fmt, tma, ctas, smem, dev, fits)
-                   : kernel_fits_fmt<2>(fmt, tma, ctas, smem, dev, fits);
+    return NT == 1 ? kernel_fits_fmt<1, kEpi>(fmt, tma, ctas, smem, dev, fits)
+                   : kernel_fits_fmt<2, kEpi>(fmt, tma, ctas, smem, dev, fits);
 }
 
 }  // namespace
@@ -681,13 +686,15 @@ size_t skinny_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, int spli
 
 int skinny_launches(int64_t M, int64_t N, int64_t K, int fmt, int split_k, const DeviceInfo &dev) {
     bool fits = false;
-    if (grid_fits(M, N, K, fmt, split_k, dev, &fits) != cudaSuccess) return -1;
+    if (grid_fits<false>(M, N, K, fmt, split_k, dev, &fits) != cudaSuccess) return -1;
     return fits ? 1 : 2;
 }
 
-cudaError_t launch_skinny(const uint16_t *x, const uint8_t *packed, const uint16_t *scales,
-                          uint16_t *y, int64_t M, int64_t N, int64_t K, int fmt, int split_k,
-                          const Workspace &ws, cudaStream_t s, const DeviceInfo &dev) {
+namespace {
+template <bool kEpi>
+cudaError_t launch(const uint16_t *x, const uint8_t *packed, const uint16_t *scales, uint16_t *y, int64_t M, int64_t N,
+                   int64_t K, int fmt, int split_k, const Workspace &ws, cudaStream_t s, const DeviceInfo &dev,
+                   const Epilogue &epi) {
     if (fmt < 1 || fmt > 4) return cudaErrorInvalidValue;
     uint16_t *xsg = reinterpret_cast<uint16_t *>(ws.data);
     float *gsg = reinterpret_cast<float *>(ws.data + staged_bytes(M, K));
@@ -723,7 +730,7 @@ cudaError_t launch_skinny(const uint16_t *x, const uint8_t *packed, const uint16
     // one launch when the whole grid is resident at once (its CTAs meet at a barrier after
     // rotating x), else the rotation pass first
     bool fits = false;
-    cudaError_t ferr = grid_fits(M, N, K, fmt, split_k, dev, &fits);
+    cudaError_t ferr = grid_fits<kEpi>(M, N, K, fmt, split_k, dev, &fits);
     if (ferr != cudaSuccess) return ferr;
     const bool fused = fits && ws.zeroed != nullptr && ws.zeroed_bytes >= kCtlRegionBytes;
     auto run = [&](auto prep, auto kern, int MT, int NT) -> cudaError_t {
@@ -733,29 +740,37 @@ cudaError_t launch_skinny(const uint16_t *x, const uint8_t *packed, const uint16
         if (!fused) prep<<<(unsigned)((G * MT + 7) / 8), 256, 0, s>>>(x, xsg, gsg, (int)M, K);
         kern<<<grid, kThreads, smem, s>>>(xsg, gsg, packed, scales, y, partials, ws.counters, (int)M, N, K, S, gpc,
                                           fused ? x : nullptr, reinterpret_cast<unsigned int *>(ws.zeroed), wmap,
-                                          smap);
+                                          smap, epi);
         return cudaGetLastError();
     };
     if (M <= 8) {
         if (fmt == 4)
-            return tma ? run(skinny_prep_kernel<8, 4>, skinny_kernel<1, 4, true>, 8, 1)
-                       : run(skinny_prep_kernel<8, 4>, skinny_kernel<1, 4, false>, 8, 1);
+            return tma ? run(skinny_prep_kernel<8, 4>, skinny_kernel<1, 4, true, kEpi>, 8, 1)
+                       : run(skinny_prep_kernel<8, 4>, skinny_kernel<1, 4, false, kEpi>, 8, 1);
         if (fmt == 3)
-            return tma ? run(skinny_prep_kernel<8, 3>, skinny_kernel<1, 3, true>, 8, 1)
-                       : run(skinny_prep_kernel<8, 3>, skinny_kernel<1, 3, false>, 8, 1);
-        if (fmt == 1) return run(skinny_prep_kernel<8, 1>, skinny_kernel<1, 1, false>, 8, 1);
-        return tma ? run(skinny_prep_kernel<8, 2>, skinny_kernel<1, 2, true>, 8, 1)
-                   : run(skinny_prep_kernel<8, 2>, skinny_kernel<1, 2, false>, 8, 1);
+            return tma ? run(skinny_prep_kernel<8, 3>, skinny_kernel<1, 3, true, kEpi>, 8, 1)
+                       : run(skinny_prep_kernel<8, 3>, skinny_kernel<1, 3, false, kEpi>, 8, 1);
+        if (fmt == 1) return run(skinny_prep_kernel<8, 1>, skinny_kernel<1, 1, false, kEpi>, 8, 1);
+        return tma ? run(skinny_prep_kernel<8, 2>, skinny_kernel<1, 2, true, kEpi>, 8, 1)
+                   : run(skinny_prep_kernel<8, 2>, skinny_kernel<1, 2, false, kEpi>, 8, 1);
     }
     if (fmt == 4)
-        return tma ? run(skinny_prep_kernel<16, 4>, skinny_kernel<2, 4, true>, 16, 2)
-                   : run(skinny_prep_kernel<16, 4>, skinny_kernel<2, 4, false>, 16, 2);
+        return tma ? run(skinny_prep_kernel<16, 4>, skinny_kernel<2, 4, true, kEpi>, 16, 2)
+                   : run(skinny_prep_kernel<16, 4>, skinny_kernel<2, 4, false, kEpi>, 16, 2);
     if (fmt == 3)
-        return tma ? run(skinny_prep_kernel<16, 3>, skinny_kernel<2, 3, true>, 16, 2)
-                   : run(skinny_prep_kernel<16, 3>, skinny_kernel<2, 3, false>, 16, 2);
-    if (fmt == 1) return run(skinny_prep_kernel<16, 1>, skinny_kernel<2, 1, false>, 16, 2);
-    return tma ? run(skinny_prep_kernel<16, 2>, skinny_kernel<2, 2, true>, 16, 2)
-               : run(skinny_prep_kernel<16, 2>, skinny_kernel<2, 2, false>, 16, 2);
+        return tma ? run(skinny_prep_kernel<16, 3>, skinny_kernel<2, 3, true, kEpi>, 16, 2)
+                   : run(skinny_prep_kernel<16, 3>, skinny_kernel<2, 3, false, kEpi>, 16, 2);
+    if (fmt == 1) return run(skinny_prep_kernel<16, 1>, skinny_kernel<2, 1, false, kEpi>, 16, 2);
+    return tma ? run(skinny_prep_kernel<16, 2>, skinny_kernel<2, 2, true, kEpi>, 16, 2)
+               : run(skinny_prep_kernel<16, 2>, skinny_kernel<2, 2, false, kEpi>, 16, 2);
+}
+}  // namespace
+
+cudaError_t launch_skinny(const uint16_t *x, const uint8_t *packed, const uint16_t *scales,
+                          uint16_t *y, int64_t M, int64_t N, int64_t K, int fmt, int split_k,
+                          const Workspace &ws, cudaStream_t s, const DeviceInfo &dev, const Epilogue *epi) {
+    return epi ? launch<true>(x, packed, scales, y, M, N, K, fmt, split_k, ws, s, dev, *epi)
+               : launch<false>(x, packed, scales, y, M, N, K, fmt, split_k, ws, s, dev, Epilogue{});
 }
 
 }  // namespace bonsai

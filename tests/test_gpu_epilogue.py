@@ -90,6 +90,19 @@ def test_epilogue_on_every_kernel(bz, kernel):
     assert bz.bonsai_device_status(clear=True) == 0
 
 
+@pytest.mark.parametrize("kernel", KERNELS, ids=lambda k: "algo%d-s%d-f%d-%dx%dx%d" % k)
+def test_no_epilogue_is_the_plain_product(bz, kernel):
+    """Without bias, activation and residual the call gives the bits of bonsai_ternary_linear_algo."""
+    import torch
+    algo, split_k, fmt, M, N, K = kernel
+    p = Problem(M, N, K, fmt, seed=M + N + K)
+    x, packed, scales = dev = p.device()
+    y = torch.empty((M, N), dtype=torch.float16, device="cuda")
+    bz.bonsai_ternary_linear_algo(x, packed, scales, y, M, N, K, fmt, algo, split_k)
+    torch.cuda.synchronize()
+    assert np.array_equal(run(bz, p, dev, None, None, 0, algo, split_k), to_numpy_f16(y))
+
+
 @pytest.mark.parametrize("fmt", [PTQ1, PQ2, Q1, G64])
 @pytest.mark.parametrize("M", [1, 2, 3, 4, 16, 17, 130])
 def test_automatic_choice(bz, fmt, M):
@@ -120,3 +133,25 @@ def test_nan_stays_nan_through_activations(bz):
             got = run(bz, p, p.device(), None, None, act, algo)
             assert np.isnan(got[M - 1]).all(), (M, act)
             assert np.isfinite(got[: M - 1]).all(), (M, act)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4000, 5120), (3, 2000, 2048), (300, 1000, 4096)])
+def test_forced_timeouts_reach_the_output(bz, M, N, K):
+    """Where a hand-over is made to give up, the epilogue leaves NaN exactly where the plain product
+    has it, and the next call is right."""
+    import torch
+    p = Problem(M, N, K, PQ2, seed=2)
+    bias, residual = inputs_of(p, 2)
+    x, packed, scales = dev = p.device()
+    y = torch.empty((M, N), dtype=torch.float16, device="cuda")
+    bz.bonsai_debug_force_timeouts(True)
+    try:
+        bz.bonsai_ternary_linear(x, packed, scales, y, M, N, K, PQ2)
+        torch.cuda.synchronize()
+        got = run(bz, p, dev, bias, residual, 1)
+    finally:
+        bz.bonsai_debug_force_timeouts(False)
+    assert np.array_equal(np.isnan(got), np.isnan(to_numpy_f16(y)))
+    assert bz.bonsai_device_status(clear=True) != 0
+    check(run(bz, p, dev, bias, residual, 1), p.oracle_y(), bias, residual, 1)
+    assert bz.bonsai_device_status(clear=True) == 0
