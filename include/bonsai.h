@@ -390,6 +390,8 @@ int bonsai_ternary_linear_noalloc(const uint16_t *x, const uint8_t *packed, cons
                                             /* phase, or a weight copy, never ended           */
 #define BONSAI_DEVICE_CACHE_RANGE 16u       /* append or attention: a slot, page or length  */
                                             /* outside the cache (no such entry was touched)  */
+#define BONSAI_DEVICE_ATTENTION_TIMEOUT 32u /* attention: a copy of keys and values never    */
+                                            /* landed                                         */
 
 /* Reads the calling device's status bits into *bits after synchronising `stream` (the
  * stream of the calls in question), and clears them when `clear` is non-zero.  *bits is 0

@@ -38,6 +38,7 @@ BONSAI_DEVICE_GEMV_PIECE_TIMEOUT = 2
 BONSAI_DEVICE_GEMM_TIMEOUT = 4
 BONSAI_DEVICE_SKINNY_TIMEOUT = 8
 BONSAI_DEVICE_CACHE_RANGE = 16
+BONSAI_DEVICE_ATTENTION_TIMEOUT = 32
 
 BONSAI_ALGO_AUTO = 0
 BONSAI_ALGO_SIMPLE = 1

@@ -572,7 +572,7 @@ int bonsai_paged_attention(const uint16_t *q, const void *k_cache, const void *v
     rc = probe_current(&dev, &st);
     if (rc != BONSAI_OK) return rc;
     Workspace ws;
-    rc = ensure_workspace(*st, attention_workspace_bytes(B, Hq, Hkv, D, st->info), 0, &ws);
+    rc = ensure_workspace(*st, attention_workspace_bytes(D, Hq / Hkv, st->info), 0, &ws);
     if (rc != BONSAI_OK) return rc;
     const KvCache c = {const_cast<void *>(k_cache), const_cast<void *>(v_cache), k_scale, v_scale, pages,
                        (int)page_size, (int)Hkv, (int)D, kv_type};

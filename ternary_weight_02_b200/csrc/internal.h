@@ -90,6 +90,7 @@ constexpr unsigned int kDevStatusGemvCopyTimeout = 1u;   // integer GEMV: a weig
 constexpr unsigned int kDevStatusGemvPieceTimeout = 2u;  // integer GEMV: a split tile's later piece never came
 constexpr unsigned int kDevStatusGemmTimeout = 4u;       // prefill GEMM: a barrier or hand-over wait gave up
 constexpr unsigned int kDevStatusCacheRange = 16u;       // append or attention: a slot, page or length outside the cache
+constexpr unsigned int kDevStatusAttentionTimeout = 32u; // attention: a copy of keys and values never landed
 constexpr unsigned int kDevStatusSkinnyTimeout = 8u;     // skinny kernel: the wait for the rotated x, or a TMA copy, gave up
 
 // ---- gemv_imma.cu: M <= 3 (g64: 2), PQ2_0 and g64, integer tensor cores
@@ -149,7 +150,7 @@ cudaError_t launch_rope_append(const uint16_t *qkv, uint16_t *q_out, const KvCac
                                const Workspace &ws, cudaStream_t s, const DeviceInfo &dev);
 
 // ---- attention.cu: one new token per sequence over a paged cache (table: B x width pages)
-size_t attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, const DeviceInfo &dev);
+size_t attention_workspace_bytes(int64_t D, int64_t G, const DeviceInfo &dev);  // G: query heads of a key head
 cudaError_t launch_paged_attention(const uint16_t *q, const KvCache &c, const int32_t *table, const int32_t *lengths,
                                    uint16_t *out, float *lse, int64_t B, int64_t Hq, int64_t ld_q, int64_t ld_out,
                                    int64_t width, int64_t window, float scale, const Workspace &ws, cudaStream_t s,
