@@ -8,16 +8,18 @@
 // it, 4 G flops per FP16 element pair, far below the tensor cores' rate.  So the design serves
 // the copies:
 //
-// * Units of work are tiles of kTile keys of one (sequence, key/value head, tile of 8 NT query
+// * Units of work are tiles of 64 or 128 keys of one (sequence, key/value head, tile of 8 NT query
 //   heads).  All units of the call lie in one list, sequence by sequence, and each CTA of a
 //   grid that is resident at once takes an equal run of it: a ragged batch loads every SM
 //   alike, one long sequence spreads over all of them, and the host needs no lengths (a
 //   captured call follows them).  Every CTA finds its run from a scan of the lengths.
 // * A producer warp walks the run's tiles, across sequences, and keeps a ring of kStages tiles
 //   in flight by TMA: one box per page and pool, 128-byte (64-byte for 64-byte rows) swizzle.
-//   Page numbers are read 32 at a time, checked, and never followed when out of range.
-// * kWarps consumer warps take 16 keys of each tile: S^T = K Q^T as m16n8k16 MMAs with the keys
-//   as rows, so that 8 query heads fill the columns and no row is wasted on padding; the
+//   Page numbers are read 32 at a time, checked, and never followed when out of range.  Three
+//   CTAs of two 32 KB stages per SM beat two of three (64 ragged sequences 82 against 86 us):
+//   the consumers' latency, not the bytes in flight, is what more of them hides.
+// * kWarps consumer warps take 16 keys of each tile (two blocks of 16 where a row has 128 bytes
+//   or fewer: E4M3 ragged 96 against 103 us): S^T = K Q^T as m16n8k16 MMAs with the keys as rows, so that 8 query heads fill the columns and no row is wasted on padding; the
 //   probabilities are rounded to FP16 (half a step of 2^-11 of each, the error of the FP16
 //   output they make), transposed by movmatrix into the B operand of O^T += V^T P^T.  Each
 //   warp keeps its own m, l and O; they meet once per piece of a run.
@@ -29,8 +31,6 @@
 //
 // Keys outside the sequence's window get a score of -infinity, and their values are masked to
 // zero in the MMA operand (a NaN there times a zero probability would be a NaN).
-#include <cuda_fp8.h>
-#include <string.h>
 
 #include "common.cuh"
 #include "internal.h"
@@ -39,19 +39,21 @@
 namespace bonsai {
 namespace {
 
-constexpr int kWarps = 4;               // consumer warps
-constexpr int kTile = 16 * kWarps;      // keys of a tile
+constexpr int kWarps = 4;  // consumer warps
 constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kMinTiles = 1;            // tiles of a CTA's run, at least
+// Parts of an item that one CTA adds up at once; more go in groups.  (131072 keys, 8 heads, 56
+// parts: 87.9 us in groups, 92.8 us at once; 1024 keys, 16 parts: 10.4 against 9.0 us.)
+constexpr int kFlatParts = 20;
 
 template <int D, int kType>
 struct Cfg {
     static constexpr int kRowBytes = kType == 0 ? 2 * D : D;
     static constexpr int kInner = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a box row
-    static constexpr int kBlocks = kRowBytes / kInner;                // 128-byte columns of a row
+    static constexpr int kBlk = kRowBytes <= 128 ? 2 : 1;             // 16-key blocks of a warp in a tile
+    static constexpr int kTile = 16 * kWarps * kBlk;                  // keys of a tile
     static constexpr int kPoolBytes = kTile * kRowBytes;              // one pool's part of a stage
     static constexpr int kStageBytes = 2 * kPoolBytes;
-    static constexpr int kStages = kStageBytes > 16384 ? 3 : kStageBytes > 8192 ? 6 : 8;
+    static constexpr int kStages = kStageBytes > 32768 ? 3 : kStageBytes > 16384 ? 2 : 4;
 };
 
 struct Layout {
@@ -111,13 +113,41 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Four E4M3 values as FP16, exactly: bytes 0, 1 in lo, bytes 2, 3 in hi.
+__device__ __forceinline__ void e4m3x4_to_half(uint32_t four, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
+}
+// 2^x, x <= 0 or -infinity: relative error 2^-22
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// Loads through L2 that are issued where they stand: several in flight before the first use.
+__device__ __forceinline__ float2 load_now(const float2 *p) {
+    float2 v;
+    asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 load_now(const float4 *p) {
+    float4 v;
+    asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+    return v;
 }
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
 // 2^(m - top), 0 for a part without keys (m = -infinity; top may be too)
-__device__ __forceinline__ float weight_of(float m, float top) { return m == -INFINITY ? 0.f : exp2f(m - top); }
+__device__ __forceinline__ float weight_of(float m, float top) { return m == -INFINITY ? 0.f : exp2_fast(m - top); }
+
+// a / b for a >= 0, b > 0: 32-bit where both fit (the 64-bit division is a long routine)
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
 
 // Keys of sequence b that take part, [first, len), and the tiles they lie in.
 struct Span {
@@ -125,6 +155,7 @@ struct Span {
     int tile0, tiles;
     bool bad;
 };
+template <int kTile>
 __device__ __forceinline__ Span span_of(const Params &p, int given) {
     Span s;
     s.bad = given < 0 || given > p.cap;
@@ -137,21 +168,22 @@ __device__ __forceinline__ Span span_of(const Params &p, int given) {
 }
 
 // A walk over a run of units: item by item, an item being (sequence, head, query tile).
+template <int kTile>
 struct Walk {
     int b, hg, t;       // sequence, (head, query tile) in it, tile of the item
     int64_t left;       // units left of the run
     int next_len;
     Span s;
     __device__ __forceinline__ void enter(const Params &p) {
-        s = span_of(p, next_len);
+        s = span_of<kTile>(p, next_len);
         next_len = b + 1 < p.B ? __ldcg(p.lengths + b + 1) : 0;
     }
-    __device__ __forceinline__ void start(const Params &p, int b0, int64_t off, int64_t units) {
+    __device__ __forceinline__ void start(const Params &p, int b0, int len0, int64_t off, int64_t units) {
         b = b0;
         left = units;
-        next_len = __ldcg(p.lengths + b);
+        next_len = len0;
         enter(p);
-        hg = (int)(off / s.tiles);
+        hg = (int)divide(off, s.tiles);
         t = (int)(off - (int64_t)hg * s.tiles);
     }
     // the piece of the current item in this run: tiles [t, end)
@@ -172,6 +204,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const __grid_consta
                                                              const __grid_constant__ CUtensorMap v_map, Params p) {
     using C = Cfg<D, kType>;
     constexpr Layout L = layout<D, kType, NT>();
+    constexpr int kTile = C::kTile, kBlk = C::kBlk;
     constexpr int kQ = 8 * NT;                 // query heads of an item
     constexpr int kSlot = kQ * (D + 2);        // floats of a partial result: O, then m, l
     constexpr bool kQRegs = NT * D <= 256;     // Q fragments in registers, else re-read per tile
@@ -182,7 +215,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const __grid_consta
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + L.bars), *empty = full + C::kStages;
     volatile int *bad_page = reinterpret_cast<int *>(empty + C::kStages);
     __shared__ int64_t scan_warp[kWarps + 1], start_off;
-    __shared__ int start_b, last_flag;
+    __shared__ int start_b, start_len, last_flag;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gid = lane >> 2, tig = lane & 3;
@@ -197,7 +230,8 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const __grid_consta
     const int per = (p.B + kThreads - 1) / kThreads;
     const int bs = tid * per < p.B ? tid * per : p.B, be = bs + per < p.B ? bs + per : p.B;
     int64_t mine = 0;
-    for (int b = bs; b < be; b++) mine += span_of(p, __ldcg(p.lengths + b)).tiles;
+    int len = 0;  // the stretch's last length
+    for (int b = bs; b < be; b++) mine += span_of<kTile>(p, len = __ldcg(p.lengths + b)).tiles;
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -212,25 +246,29 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const __grid_consta
         tiles += scan_warp[w];
     }
     const int64_t HG = (int64_t)p.Hkv * p.GT, W = tiles * HG;
-    const int64_t want = (W + kMinTiles - 1) / kMinTiles;
-    const int64_t nc = want < (int64_t)gridDim.x ? want : (int64_t)gridDim.x;  // CTAs with work
+    const int64_t nc = W < (int64_t)gridDim.x ? W : (int64_t)gridDim.x;  // CTAs with work
     const int64_t cta = blockIdx.x;
     if (cta >= nc) return;
-    const int64_t w0 = W * cta / nc, w1 = W * (cta + 1) / nc;
+    const int64_t w0 = divide(W * cta, nc), w1 = divide(W * (cta + 1), nc);
     if (w0 >= before * HG && w0 < (before + mine) * HG) {  // one thread: the run starts in its stretch
         int64_t at = before * HG;
         int b = bs;
-        for (;; b++) {
-            const int64_t n = span_of(p, __ldcg(p.lengths + b)).tiles * HG;
-            if (w0 < at + n) break;
+        for (; be - b > 1; b++) {  // (the last is the one whose length is at hand)
+            const int v = __ldcg(p.lengths + b);
+            const int64_t n = span_of<kTile>(p, v).tiles * HG;
+            if (w0 < at + n) {
+                len = v;
+                break;
+            }
             at += n;
         }
         start_b = b;
+        start_len = len;
         start_off = w0 - at;
     }
     __syncthreads();
-    Walk walk;
-    walk.start(p, start_b, start_off, w1 - w0);
+    Walk<kTile> walk;
+    walk.start(p, start_b, start_len, start_off, w1 - w0);
     const int slab = 1 << p.page_shift < kTile ? 1 << p.page_shift : kTile;  // keys of a box
 
     if (warp == kWarps) {
@@ -294,16 +332,28 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const __grid_consta
     }
 
     // -------------------------------------------------------------------- consumers
-    // ldmatrix addresses of this lane in a slab: key row and 16-byte chunk of the four matrices
+    // ldmatrix addresses: matrix mi of four, row r8 of its eight.  A row's 16-byte chunk c lies in
+    // 128-byte block c / 8 (each `slab` rows tall), at place c % 8 xored with the row's swizzle
+    // bits; as nothing else sets those address bits, the xor takes the whole address.
     const int mi = lane >> 3, r8 = lane & 7;
     const int key_k = r8 + (mi & 1) * 8, chunk_k = mi >> 1;
     const int key_v = r8 + (kType == 0 ? (mi >> 1) * 8 : (mi & 1) * 8), chunk_v = kType == 0 ? (mi & 1) : (mi >> 1);
-    const int row0 = (16 * warp) & (slab - 1), slab_off = (16 * warp) / slab * slab * C::kRowBytes;
-    auto chunk_addr = [&](uint32_t base, int key, int c) -> uint32_t {
-        // chunk c of the row: 128-byte block c / 8 (each `slab` rows tall), swizzled by the row
-        const int blk = C::kInner == 128 ? c >> 3 : 0, cc = C::kInner == 128 ? c & 7 : c;
-        const int row = row0 + key, x = C::kInner == 128 ? row & 7 : (row >> 1) & 3;
-        return base + blk * slab * C::kInner + row * C::kInner + ((cc ^ x) << 4);
+    // block j of this warp: keys 64 j + 16 warp .. + 15 of the tile, within one slab
+    auto lane_off = [&](int j, int key, int chunk) -> uint32_t {
+        const int first = 16 * (j * kWarps + warp), row = (first & (slab - 1)) + key;
+        const int x = C::kInner == 128 ? row & 7 : (row >> 1) & 3;
+        return (uint32_t)(first / slab * slab * C::kRowBytes + row * C::kInner + ((chunk ^ x) << 4));
+    };
+    uint32_t off_k[kBlk], off_v[kBlk];
+#pragma unroll
+    for (int j = 0; j < kBlk; j++) {
+        off_k[j] = lane_off(j, key_k, chunk_k);
+        off_v[j] = C::kPoolBytes + lane_off(j, key_v, chunk_v);
+    }
+    const uint32_t block_bytes = slab * C::kInner;
+    auto chunk_addr = [&](uint32_t base, int c) -> uint32_t {  // c even
+        constexpr int kChunks = C::kInner / 16;
+        return (base ^ ((c & (kChunks - 1)) << 4)) + (c / kChunks) * block_bytes;
     };
     bool alive = true;
     int st = 0;
@@ -357,61 +407,87 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const __grid_consta
                 continue;
             }
             nan = nan || bad_page[st] != 0;
-            const uint32_t kb = saddr(smem + st * C::kStageBytes) + slab_off, vb = kb + C::kPoolBytes;
+            const uint32_t stage = saddr(smem + st * C::kStageBytes);
             const int64_t key0 = (int64_t)(s.tile0 + t) * kTile + 16 * warp;
-            if (key0 < s.len && key0 + 16 > s.first) {  // (uniform in the warp) it has keys here
-                float z[NT][4];
+            constexpr int kStep = 16 * kWarps;  // keys between a warp's blocks
+            if (key0 < s.len && key0 + (kBlk - 1) * kStep + 16 > s.first) {  // (uniform in the warp) it has keys here
+                float z[kBlk][NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; nt++) z[nt][0] = z[nt][1] = z[nt][2] = z[nt][3] = 0.f;
-                auto score = [&](int ks, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+                for (int j = 0; j < kBlk; j++)
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++) z[j][nt][0] = z[j][nt][1] = z[j][nt][2] = z[j][nt][3] = 0.f;
+                auto score = [&](int j, int ks, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++) {
                         if constexpr (kQRegs) {
-                            mma16816(z[nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+                            mma16816(z[j][nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
                         } else {
                             uint32_t b0, b1;
                             load_q(nt, ks, b0, b1);
-                            mma16816(z[nt], a0, a1, a2, a3, b0, b1);
+                            mma16816(z[j][nt], a0, a1, a2, a3, b0, b1);
                         }
                     }
                 };
                 if (kType == 0) {
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ks++) {
-                        uint32_t a[4];
-                        ldmatrix4(a, chunk_addr(kb, key_k, 2 * ks + chunk_k));
-                        score(ks, a[0], a[1], a[2], a[3]);
-                    }
+                    for (int ks = 0; ks < D / 16; ks++)
+#pragma unroll
+                        for (int j = 0; j < kBlk; j++) {
+                            uint32_t a[4];
+                            ldmatrix4(a, chunk_addr(stage + off_k[j], 2 * ks));
+                            score(j, ks, a[0], a[1], a[2], a[3]);
+                        }
                 } else {
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ks += 2) {  // 16-byte chunks ks, ks + 1 of rows gid, gid + 8
-                        uint32_t a[4];
-                        ldmatrix4(a, chunk_addr(kb, key_k, ks + chunk_k));
+                    for (int ks = 0; ks < D / 16; ks += 2)  // 16-byte chunks ks, ks + 1 of rows gid, gid + 8
 #pragma unroll
-                        for (int i = 0; i < 2; i++)
-                            score(ks + i, e4m3x2_to_half2(a[2 * i] & 0xffffu), e4m3x2_to_half2(a[2 * i + 1] & 0xffffu),
-                                  e4m3x2_to_half2(a[2 * i] >> 16), e4m3x2_to_half2(a[2 * i + 1] >> 16));
+                        for (int j = 0; j < kBlk; j++) {
+                            uint32_t a[4];
+                            ldmatrix4(a, chunk_addr(stage + off_k[j], ks));
+#pragma unroll
+                            for (int i = 0; i < 2; i++) {
+                                uint32_t a0, a1, a2, a3;
+                                e4m3x4_to_half(a[2 * i], a0, a2);
+                                e4m3x4_to_half(a[2 * i + 1], a1, a3);
+                                score(j, ks + i, a0, a1, a2, a3);
+                            }
+                        }
+                }
+                // keys gid and gid + 8 of a block's scores; keys 2 tig (+ 1, + 8, + 9) of its values
+                const bool edge = key0 < s.first || key0 + (kBlk - 1) * kStep + 16 > s.len;
+                uint32_t vm[kBlk][2];
+#pragma unroll
+                for (int j = 0; j < kBlk; j++) vm[j][0] = vm[j][1] = 0xffffffffu;
+#pragma unroll
+                for (int j = 0; j < kBlk; j++)
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++) z[j][nt][e] *= to2;
+                if (edge) {
+#pragma unroll
+                    for (int j = 0; j < kBlk; j++) {
+                        const int64_t kj = key0 + j * kStep;
+                        auto in = [&](int i) { return kj + i >= s.first && kj + i < s.len; };
+                        const bool in0 = in(gid), in1 = in(gid + 8);
+                        vm[j][0] = (in(2 * tig) ? 0xffffu : 0u) | (in(2 * tig + 1) ? 0xffff0000u : 0u);
+                        vm[j][1] = (in(2 * tig + 8) ? 0xffffu : 0u) | (in(2 * tig + 9) ? 0xffff0000u : 0u);
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                            for (int e = 0; e < 4; e++)
+                                if (!(e < 2 ? in0 : in1)) z[j][nt][e] = -INFINITY;
                     }
                 }
-                // keys gid and gid + 8 of this lane's scores; keys 2 tig (+ 1, + 8, + 9) of its values
-                const bool edge = key0 < s.first || key0 + 16 > s.len;
-                uint32_t vm0 = 0xffffffffu, vm1 = 0xffffffffu;
-                bool in0 = true, in1 = true;
-                if (edge) {
-                    auto in = [&](int j) { return key0 + j >= s.first && key0 + j < s.len; };
-                    in0 = in(gid), in1 = in(gid + 8);
-                    vm0 = (in(2 * tig) ? 0xffffu : 0u) | (in(2 * tig + 1) ? 0xffff0000u : 0u);
-                    vm1 = (in(2 * tig + 8) ? 0xffffu : 0u) | (in(2 * tig + 9) ? 0xffff0000u : 0u);
-                }
-                uint32_t pb[NT][2];
+                uint32_t pb[kBlk][NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++) {
-#pragma unroll
-                    for (int e = 0; e < 4; e++) z[nt][e] = (e < 2 ? in0 : in1) ? z[nt][e] * to2 : -INFINITY;
                     float top[2];
 #pragma unroll
                     for (int e = 0; e < 2; e++) {
-                        float v = fmaxf(z[nt][e], z[nt][e + 2]);
+                        float v = fmaxf(z[0][nt][e], z[0][nt][e + 2]);
+#pragma unroll
+                        for (int j = 1; j < kBlk; j++) v = fmaxf(v, fmaxf(z[j][nt][e], z[j][nt][e + 2]));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
@@ -429,38 +505,46 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const __grid_consta
                     }
                     // (a maximum of -infinity, every score being one: 2^(-inf - 0) = 0)
                     const float s0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], s1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-                    const float p0 = exp2f(z[nt][0] - s0), p1 = exp2f(z[nt][1] - s1), p2 = exp2f(z[nt][2] - s0),
-                                p3 = exp2f(z[nt][3] - s1);
-                    l[nt][0] += p0 + p2;
-                    l[nt][1] += p1 + p3;
-                    const __half2 h01 = __floats2half2_rn(p0, p1), h23 = __floats2half2_rn(p2, p3);
-                    pb[nt][0] = transpose8x8(*reinterpret_cast<const uint32_t *>(&h01));
-                    pb[nt][1] = transpose8x8(*reinterpret_cast<const uint32_t *>(&h23));
-                }
-                auto weigh = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-                    if (edge) a0 &= vm0, a1 &= vm0, a2 &= vm1, a3 &= vm1;
 #pragma unroll
-                    for (int nt = 0; nt < NT; nt++) mma16816(o[nt][i], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                    for (int j = 0; j < kBlk; j++) {
+                        const float p0 = exp2_fast(z[j][nt][0] - s0), p1 = exp2_fast(z[j][nt][1] - s1);
+                        const float p2 = exp2_fast(z[j][nt][2] - s0), p3 = exp2_fast(z[j][nt][3] - s1);
+                        l[nt][0] += p0 + p2;
+                        l[nt][1] += p1 + p3;
+                        const __half2 h01 = __floats2half2_rn(p0, p1), h23 = __floats2half2_rn(p2, p3);
+                        pb[j][nt][0] = transpose8x8(*reinterpret_cast<const uint32_t *>(&h01));
+                        pb[j][nt][1] = transpose8x8(*reinterpret_cast<const uint32_t *>(&h23));
+                    }
+                }
+                auto weigh = [&](int j, int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+                    if (edge) a0 &= vm[j][0], a1 &= vm[j][0], a2 &= vm[j][1], a3 &= vm[j][1];
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++) mma16816(o[nt][i], a0, a1, a2, a3, pb[j][nt][0], pb[j][nt][1]);
                 };
                 if (kType == 0) {
 #pragma unroll
-                    for (int i = 0; i < D / 16; i++) {
-                        uint32_t a[4];
-                        ldmatrix4_trans(a, chunk_addr(vb, key_v, 2 * i + chunk_v));
-                        weigh(i, a[0], a[1], a[2], a[3]);
-                    }
+                    for (int j = 0; j < kBlk; j++)
+#pragma unroll
+                        for (int i = 0; i < D / 16; i++) {
+                            uint32_t a[4];
+                            ldmatrix4_trans(a, chunk_addr(stage + off_v[j], 2 * i));
+                            weigh(j, i, a[0], a[1], a[2], a[3]);
+                        }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < D / 16; i += 2) {
-                        uint32_t a[4];
-                        ldmatrix4_trans(a, chunk_addr(vb, key_v, i + chunk_v));
+                    for (int j = 0; j < kBlk; j++)
 #pragma unroll
-                        for (int j = 0; j < 2; j++) {  // bytes (0, 2): dimension 2 gid, (1, 3): 2 gid + 1
-                            const uint32_t x = __byte_perm(a[2 * j], 0, 0x3120), y = __byte_perm(a[2 * j + 1], 0, 0x3120);
-                            weigh(i + j, e4m3x2_to_half2(x & 0xffffu), e4m3x2_to_half2(x >> 16),
-                                  e4m3x2_to_half2(y & 0xffffu), e4m3x2_to_half2(y >> 16));
+                        for (int i = 0; i < D / 16; i += 2) {
+                            uint32_t a[4];
+                            ldmatrix4_trans(a, chunk_addr(stage + off_v[j], i));
+#pragma unroll
+                            for (int u = 0; u < 2; u++) {  // bytes (0, 2): dimension 2 gid, (1, 3): 2 gid + 1
+                                uint32_t a0, a1, a2, a3;
+                                e4m3x4_to_half(__byte_perm(a[2 * u], 0, 0x3120), a0, a1);
+                                e4m3x4_to_half(__byte_perm(a[2 * u + 1], 0, 0x3120), a2, a3);
+                                weigh(j, i + u, a0, a1, a2, a3);
+                            }
                         }
-                    }
                 }
             }
             // this warp's reads of the stage come before the copies that refill it
@@ -571,41 +655,95 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const __grid_consta
             }
             // CTAs of the item's first and last unit: unit u lies in CTA ((u + 1) nc - 1) / W
             const int64_t u0 = w1 - walk.left - walk.t, u1 = u0 + s.tiles - 1;
-            const int64_t c_first = ((u0 + 1) * nc - 1) / W, c_last = ((u1 + 1) * nc - 1) / W;
-            __threadfence();
-            consumers_sync();
-            if (tid == 0) last_flag = atomicAdd(p.counters + c_first, 1u) == (unsigned int)(c_last - c_first);
-            consumers_sync();
-            if (last_flag) {
-                __threadfence();
-                if (tid == 0) p.counters[c_first] = 0u;  // for the next call
-                auto slot_of = [&](int64_t c) { return p.partials + (2 * c + (c == c_first ? 1 : 0)) * kSlot; };
+            const int c_first = (int)divide((u0 + 1) * nc - 1, W), parts = (int)divide((u1 + 1) * nc - 1, W) - c_first + 1;
+            auto slot_no = [&](int k) { return 2 * (c_first + k) + (k == 0 ? 1 : 0); };
+            auto slot_at = [&](int k) { return p.partials + (int64_t)slot_no(k) * kSlot; };
+            // counts this CTA's arrival; true for the last of `total`, which then sees all they wrote
+            auto arrive = [&](unsigned int *counter, int total) -> bool {
+                consumers_sync();
+                if (tid == 0) {
+                    unsigned int old;
+                    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+                    last_flag = old == (unsigned int)(total - 1);
+                    if (last_flag) *counter = 0u;  // for the next call
+                }
+                consumers_sync();
+                return last_flag != 0;
+            };
+            // parts k0, k0 + step, .. below k1 of n-tile nt in one pass, kAhead of them read at a time:
+            // running maximum and sums of the parts, as for the keys
+            auto add_parts = [&](int k0, int k1, int step, int nt, float2 &top, float2 &lt, float4 (&acc)[kPer]) {
+                constexpr int kAhead = 16 / kPer;
+                const int qi = nt * 8 + 2 * tig;
+                top = make_float2(-INFINITY, -INFINITY), lt = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int nt = 0; nt < NT; nt++) {
-                    const int qi = nt * 8 + 2 * tig;
-                    float2 top = make_float2(-INFINITY, -INFINITY), lt = make_float2(0.f, 0.f);
-#pragma unroll 4
-                    for (int64_t c = c_first; c <= c_last; c++) {
-                        const float2 mm = __ldcg(reinterpret_cast<const float2 *>(slot_of(c) + kQ * D + qi));
-                        top.x = fmaxf(top.x, mm.x), top.y = fmaxf(top.y, mm.y);
+                for (int j = 0; j < kPer; j++) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = k0; k < k1; k += kAhead * step) {
+                    float2 mm[kAhead], ll[kAhead];
+                    float4 v[kAhead][kPer];
+#pragma unroll
+                    for (int u = 0; u < kAhead; u++) {  // (past the last: the first again, without weight)
+                        const float *sp = slot_at(k + u * step < k1 ? k + u * step : k0);
+                        mm[u] = load_now(reinterpret_cast<const float2 *>(sp + kQ * D + qi));
+                        ll[u] = load_now(reinterpret_cast<const float2 *>(sp + kQ * D + kQ + qi));
+#pragma unroll
+                        for (int j = 0; j < kPer; j++)
+                            v[u][j] = load_now(reinterpret_cast<const float4 *>(sp) +
+                                               (nt * (D / 16) + j * kWarps + warp) * 32 + lane);
                     }
-                    float4 acc[kPer];
 #pragma unroll
-                    for (int j = 0; j < kPer; j++) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int64_t c = c_first; c <= c_last; c++) {
-                        const float *sp = slot_of(c);
-                        const float2 mm = __ldcg(reinterpret_cast<const float2 *>(sp + kQ * D + qi));
-                        const float2 ll = __ldcg(reinterpret_cast<const float2 *>(sp + kQ * D + kQ + qi));
-                        const float f0 = weight_of(mm.x, top.x), f1 = weight_of(mm.y, top.y);
-                        lt.x += ll.x * f0, lt.y += ll.y * f1;
+                    for (int u = 0; u < kAhead; u++) {
+                        if (k + u * step >= k1) mm[u] = make_float2(-INFINITY, -INFINITY), ll[u] = make_float2(0.f, 0.f);
+                        const float2 t2 = make_float2(fmaxf(top.x, mm[u].x), fmaxf(top.y, mm[u].y));
+                        const float g0 = weight_of(top.x, t2.x), g1 = weight_of(top.y, t2.y);
+                        const float f0 = weight_of(mm[u].x, t2.x), f1 = weight_of(mm[u].y, t2.y);
+                        top = t2;
+                        lt.x = lt.x * g0 + ll[u].x * f0, lt.y = lt.y * g1 + ll[u].y * f1;
 #pragma unroll
                         for (int j = 0; j < kPer; j++) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(sp) +
-                                                    (nt * (D / 16) + j * kWarps + warp) * 32 + lane);
-                            acc[j].x += v.x * f0, acc[j].y += v.y * f1, acc[j].z += v.z * f0, acc[j].w += v.w * f1;
+                            acc[j].x = acc[j].x * g0 + v[u][j].x * f0, acc[j].y = acc[j].y * g1 + v[u][j].y * f1;
+                            acc[j].z = acc[j].z * g0 + v[u][j].z * f0, acc[j].w = acc[j].w * g1 + v[u][j].w * f1;
                         }
                     }
+                }
+            };
+            // Few parts: the last CTA of the item adds them all.  Many: in groups of about their
+            // root, each added by its last CTA into the slot of its first part, then the groups
+            // (one CTA reads 8 parts of 128 x 8 in about 1.1 us; a level costs about 1 us more).
+            int group = parts;
+            if (parts > kFlatParts) {
+                group = (int)ceilf(sqrtf((float)parts));
+                const int k0 = ((int)cta - c_first) / group * group, k1 = k0 + group < parts ? k0 + group : parts;
+                if (arrive(p.counters + slot_no(k0), k1 - k0)) {
+                    float2 top[NT], lt[NT];
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++) {
+                        float4 acc[kPer];
+                        add_parts(k0, k1, 1, nt, top[nt], lt[nt], acc);
+#pragma unroll
+                        for (int j = 0; j < kPer; j++)
+                            reinterpret_cast<float4 *>(slot_at(k0))[(nt * (D / 16) + j * kWarps + warp) * 32 + lane] = acc[j];
+                    }
+                    consumers_sync();  // every warp has read the first part's m and l
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++)
+                        if (warp == 0 && gid == 0) {
+                            float *sp = slot_at(k0) + kQ * D + nt * 8 + 2 * tig;
+                            *reinterpret_cast<float2 *>(sp) = top[nt];
+                            *reinterpret_cast<float2 *>(sp + kQ) = lt[nt];
+                        }
+                } else {
+                    group = 0;  // nothing more to do here
+                }
+            }
+            const int groups = group == 0 ? 0 : group == parts ? parts : (parts + group - 1) / group;
+            if (groups > 0 && arrive(p.counters + 2 * gridDim.x + c_first, groups)) {
+                const int step = group == parts ? 1 : group;
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) {
+                    float2 top, lt;
+                    float4 acc[kPer];
+                    add_parts(0, parts, step, nt, top, lt, acc);
 #pragma unroll
                     for (int j = 0; j < kPer; j++) store(nt, j, acc[j], lt);
                     store_lse(nt, top, lt);
@@ -629,10 +767,10 @@ cudaError_t prepare(int *per_sm) {
 constexpr int kMaxCtasPerSm = 4;
 
 // A pool as rows of kInner bytes: (byte, place in the page, 128-byte block, page and head).
-cudaError_t encode_pool(CUtensorMap *map, const void *pool, const KvCache &c, int row_bytes, int inner) {
+cudaError_t encode_pool(CUtensorMap *map, const void *pool, const KvCache &c, int row_bytes, int inner, int tile) {
     EncodeTiledFn encode = encode_fn();
     if (!encode) return cudaErrorNotSupported;
-    const int slab = c.page_size < kTile ? c.page_size : kTile;
+    const int slab = c.page_size < tile ? c.page_size : tile;
     const cuuint64_t dims[4] = {(cuuint64_t)inner, (cuuint64_t)c.page_size, (cuuint64_t)(row_bytes / inner),
                                 (cuuint64_t)(c.pages * c.kv_heads)};
     const cuuint64_t strides[3] = {(cuuint64_t)row_bytes, (cuuint64_t)inner, (cuuint64_t)row_bytes * c.page_size};
@@ -649,8 +787,8 @@ template <int D, int kType, int NT>
 cudaError_t launch(Params &p, const KvCache &c, cudaStream_t s, const DeviceInfo &dev) {
     using C = Cfg<D, kType>;
     CUtensorMap k_map, v_map;
-    cudaError_t e = encode_pool(&k_map, c.k, c, C::kRowBytes, C::kInner);
-    if (e == cudaSuccess) e = encode_pool(&v_map, c.v, c, C::kRowBytes, C::kInner);
+    cudaError_t e = encode_pool(&k_map, c.k, c, C::kRowBytes, C::kInner, C::kTile);
+    if (e == cudaSuccess) e = encode_pool(&v_map, c.v, c, C::kRowBytes, C::kInner, C::kTile);
     int per_sm = 0;
     if (e == cudaSuccess) e = prepare<D, kType, NT>(&per_sm);
     if (e != cudaSuccess) return e;
@@ -682,7 +820,7 @@ cudaError_t launch_paged_attention(const uint16_t *q, const KvCache &c, const in
                                    int64_t width, int64_t window, float scale, const Workspace &ws, cudaStream_t s,
                                    const DeviceInfo &dev) {
     const int64_t G = Hq / c.kv_heads;
-    if (ws.data_bytes < attention_workspace_bytes(c.head_dim, G, dev) || dev.sm_count * kMaxCtasPerSm > kMaxTiles)
+    if (ws.data_bytes < attention_workspace_bytes(c.head_dim, G, dev) || 3 * dev.sm_count * kMaxCtasPerSm > kMaxTiles)
         return cudaErrorInvalidValue;
     Params p = {};
     p.q = q;
