@@ -133,9 +133,9 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
+    if stream is None:  # the current stream's handle, without a Stream object (3 us of a call's host time)
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -268,21 +268,27 @@ def _dev(t, dtype, numel: int, dev: int, contiguous: bool = True):
 def _rows(t, rows: int, width: int, ld, dev: int):
     """(pointer, row stride) of a matrix of heads: `rows` rows of `width` FP16 elements, at the row
     stride given or the tensor's own (a contiguous tensor, or a matrix with contiguous rows)."""
-    import torch
     if t is None or type(t) is int:
         return t, width if ld is None else ld
-    if ld is None:
-        if t.is_contiguous():
-            ld = t.numel() // rows if rows > 1 else max(width, 8)
-        elif t.dim() == 2 and t.stride(1) == 1:
+    import torch
+    if t.get_device() != dev:
+        raise ValueError("tensor arguments must be CUDA tensors on the current device")
+    if t.dtype is not torch.float16:
+        raise ValueError(f"a tensor argument is {t.dtype} where torch.float16 is expected")
+    n = t.numel()
+    if t.is_contiguous():
+        if ld is None:
+            ld = width if n == rows * width or rows == 0 else n // rows
+        if n < (rows - 1) * ld + width:
+            raise ValueError("a tensor of heads is smaller than the call takes")
+    elif t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError("a strided tensor of heads is a matrix with contiguous rows")
+    else:
+        if ld is None:
             ld = t.stride(0)
-        else:
-            raise ValueError("a strided tensor of heads is a matrix with contiguous rows")
-    if t.dim() == 2 and t.stride(1) == 1 and not t.is_contiguous():
         if t.shape[0] < rows or t.shape[1] < width or t.stride(0) != ld:
             raise ValueError("a strided tensor of heads is smaller than the call takes")
-        return _dev(t, torch.float16, 0, dev, False), ld
-    return _dev(t, torch.float16, (rows - 1) * ld + width if rows > 0 else 0, dev), ld
+    return t.data_ptr(), ld
 
 
 def bonsai_ternary_linear_epilogue(x, packed, scales, bias, residual, y, M: int, N: int, K: int, fmt: int,

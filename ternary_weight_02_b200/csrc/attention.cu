@@ -19,10 +19,11 @@
 //   CTAs of two 32 KB stages per SM beat two of three (64 ragged sequences 82 against 86 us):
 //   the consumers' latency, not the bytes in flight, is what more of them hides.
 // * kWarps consumer warps take 16 keys of each tile (two blocks of 16 where a row has 128 bytes
-//   or fewer: E4M3 ragged 96 against 103 us): S^T = K Q^T as m16n8k16 MMAs with the keys as rows, so that 8 query heads fill the columns and no row is wasted on padding; the
-//   probabilities are rounded to FP16 (half a step of 2^-11 of each, the error of the FP16
-//   output they make), transposed by movmatrix into the B operand of O^T += V^T P^T.  Each
-//   warp keeps its own m, l and O; they meet once per piece of a run.
+//   or fewer: E4M3 ragged 96 against 103 us): S^T = K Q^T as m16n8k16 MMAs with the keys as
+//   rows, so that 8 query heads fill the columns and no row is wasted on padding; the
+//   probabilities are rounded to FP16 (2^-11 of each at most, the size of the output's own
+//   rounding), transposed by movmatrix into the B operand of O^T += V^T P^T.  Each warp keeps
+//   its own m, l and O; they meet once per piece of a run.
 // * E4M3 entries become FP16 in registers (exactly); the per-head scales go into the score
 //   scale and the output.  The contraction indices are taken in the order in which the bytes
 //   arrive, Q being loaded in the same order.
@@ -754,17 +755,29 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const __grid_consta
     }
 }
 
-// Resident CTAs per SM of an instance (host).
+constexpr int kMaxDevices = 64, kMaxCtasPerSm = 4;
+
+// Sets an instance up on the current device and gives its resident CTAs per SM (both are properties
+// of the instance and the device, looked up once; callers hold the library's lock).
 template <int D, int kType, int NT>
 cudaError_t prepare(int *per_sm) {
-    constexpr int smem = layout<D, kType, NT>().total;
-    auto kern = attention_kernel<D, kType, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, kern, kThreads, smem);
+    static int known[kMaxDevices];
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+    if (known[dev] == 0) {
+        constexpr int smem = layout<D, kType, NT>().total;
+        auto kern = attention_kernel<D, kType, NT>;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        int n = 0;
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, smem);
+        if (e != cudaSuccess) return e;
+        if (n < 1) return cudaErrorInvalidConfiguration;
+        known[dev] = n < kMaxCtasPerSm ? n : kMaxCtasPerSm;
+    }
+    *per_sm = known[dev];
+    return cudaSuccess;
 }
-
-constexpr int kMaxCtasPerSm = 4;
 
 // A pool as rows of kInner bytes: (byte, place in the page, 128-byte block, page and head).
 cudaError_t encode_pool(CUtensorMap *map, const void *pool, const KvCache &c, int row_bytes, int inner, int tile) {
@@ -792,8 +805,6 @@ cudaError_t launch(Params &p, const KvCache &c, cudaStream_t s, const DeviceInfo
     int per_sm = 0;
     if (e == cudaSuccess) e = prepare<D, kType, NT>(&per_sm);
     if (e != cudaSuccess) return e;
-    if (per_sm < 1) return cudaErrorInvalidConfiguration;
-    per_sm = per_sm < kMaxCtasPerSm ? per_sm : kMaxCtasPerSm;
     p.GT = (p.G + 8 * NT - 1) / (8 * NT);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(per_sm * dev.sm_count));

@@ -328,35 +328,62 @@ __device__ __forceinline__ unsigned int ld_acquire_u32(const unsigned int *p) {
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
-// Bias, activation and residual on 32 consecutive columns n0 .. n0 + 31 of row m (FP32 bits in v).
-// Columns past N and rows past M belong to no output and are left as they are.
-__device__ __forceinline__ void epilogue_row32(uint32_t *v, const Epilogue &e, int64_t m, int64_t M, int64_t n0,
-                                               int64_t N) {
-    if (m >= M || n0 >= N) return;
-    if (n0 + 32 <= N && (N & 7) == 0) {
-        uint4 b[4], r[4];
+// Residual of one warp's 32 rows x 128 columns into its staging rows (16-byte chunks swizzled by
+// the row), two rows of 256 bytes per instruction: a lane later finds its own row's values there,
+// wherever the row starts in memory.  Rows past M and columns past N get zeros.
+__device__ __forceinline__ void stage_residual(uint8_t *stage, const uint16_t *residual, int64_t m0, int64_t M,
+                                               int64_t n0, int64_t N, int lane) {
+    const int ch = lane & 15;
+    const int64_t n = n0 + ch * 8;
+    auto put = [&](int row, uint4 w) { *reinterpret_cast<uint4 *>(stage + row * 256 + ((ch ^ (row & 7)) << 4)) = w; };
+    if ((N & 7) == 0) {  // rows start on 16 bytes, and no chunk crosses N
+#pragma unroll 1
+        for (int i0 = 0; i0 < 16; i0 += 8) {
+            uint4 w[8];
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            if (e.bias) b[j] = __ldcg(reinterpret_cast<const uint4 *>(e.bias + n0) + j);
-            if (e.residual) r[j] = __ldcg(reinterpret_cast<const uint4 *>(e.residual + m * N + n0) + j);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const uint32_t bw[4] = {b[j].x, b[j].y, b[j].z, b[j].w}, rw[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
-#pragma unroll
-            for (int k = 0; k < 8; k++) {
-                float z = __uint_as_float(v[8 * j + k]);
-                if (e.bias) z += half_bits_to_float((uint16_t)(bw[k >> 1] >> (16 * (k & 1))));
-                z = activate(z, e.act);
-                if (e.residual) z += half_bits_to_float((uint16_t)(rw[k >> 1] >> (16 * (k & 1))));
-                v[8 * j + k] = __float_as_uint(z);
+            for (int i = 0; i < 8; i++) {
+                const int64_t m = m0 + 2 * (i0 + i) + (lane >> 4);
+                w[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (m < M && n < N) w[i] = __ldcg(reinterpret_cast<const uint4 *>(residual + m * N + n));
             }
-        }
-        return;
-    }
 #pragma unroll
-    for (int k = 0; k < 32; k++)
-        if (n0 + k < N) v[k] = __float_as_uint(epilogue_value(__uint_as_float(v[k]), e, m, n0 + k, N));
+            for (int i = 0; i < 8; i++) put(2 * (i0 + i) + (lane >> 4), w[i]);
+        }
+    } else {
+#pragma unroll 1
+        for (int i0 = 0; i0 < 16; i0 += 4) {
+            uint32_t h[4][8];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int64_t m = m0 + 2 * (i0 + i) + (lane >> 4);
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    h[i][e] = 0u;
+                    if (m < M && n + e < N) h[i][e] = (uint32_t)__ldcg(residual + m * N + n + e);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                put(2 * (i0 + i) + (lane >> 4), make_uint4(h[i][0] | (h[i][1] << 16), h[i][2] | (h[i][3] << 16),
+                                                          h[i][4] | (h[i][5] << 16), h[i][6] | (h[i][7] << 16)));
+        }
+    }
+    __syncwarp();
+}
+
+// bias (lane k holds column k's) and activation on 32 columns of FP32 bits
+__device__ __forceinline__ void bias_activate32(uint32_t (&v)[32], float bias, bool biased, int act) {
+    if (biased)
+#pragma unroll
+        for (int k = 0; k < 32; k++) v[k] = __float_as_uint(__uint_as_float(v[k]) + __shfl_sync(0xffffffffu, bias, k));
+    auto all = [&](auto f) {
+#pragma unroll
+        for (int k = 0; k < 32; k++) v[k] = __float_as_uint(f(__uint_as_float(v[k])));
+    };
+    if (act == 1) all([](float z) { return activate(z, 1); });
+    if (act == 2) all([](float z) { return activate(z, 2); });
+    if (act == 3) all([](float z) { return activate(z, 3); });
+    if (act == 4) all([](float z) { return activate(z, 4); });
 }
 
 // The eight expansion/epilogue warps (256 threads) meet here; barrier 0 is __syncthreads.
@@ -407,7 +434,8 @@ __device__ __forceinline__ void expand_warps_sync() { asm volatile("bar.sync 1, 
 // tiles, whose x' traffic per MMA it shares, so halving the expansion buys nothing there.
 // kEpi: bias, activation and residual of `epi` on the FP32 sums, in registers before the one
 // rounding to FP16 (never with kSwiglu or kPair).  A thread holds 32 consecutive columns of one
-// row there: it reads their residual as four 16-byte loads where rows are 16-byte aligned.
+// row there; the residual comes to it through the staging rows that y leaves by, so that both
+// move in whole rows.
 template <int kFmt, int kAcc, bool kSwiglu, bool kPair, bool kEpi = false>
 __global__ void __launch_bounds__(kThreads, 1) gemm_tcgen05_kernel(
     const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap w_map,
@@ -759,6 +787,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tcgen05_kernel(
                                       : (int64_t)tn * BN + rb;  // weight row
             // (SwiGLU: the last tile's gate rows past F belong to no output; their weights read as 0)
             const bool valid = kSwiglu ? (int64_t)tn * (BN / 2) + (rb & (BN / 2 - 1)) < F : n < N;
+            if constexpr (kEpi) {
+                // the residual of a tile that this CTA will write comes to the L2 while it computes:
+                // one row of the tile per thread, four 128-byte lines
+                const int64_t m = (int64_t)tm * kTileRows + r;
+                if (epi.residual && p.kb == 0 && r < kTileRows && m < M)
+                    for (int64_t c = (int64_t)tn * BN; c < (int64_t)tn * BN + BN && c < N; c += 64)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(epi.residual + m * N + c));
+            }
             if (live) {
                 // PTQ1_0, Q1_0: the packed bytes of the group being expanded and of the next one (in
                 // flight) come by plain loads; PQ2_0: the codes come with the stage's x' tiles
@@ -966,6 +1002,67 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tcgen05_kernel(
             uint8_t *stage_y = sB + w8 * 8192;
 #pragma unroll 1
             for (int a = 0; a < kAcc; a++) {
+                if constexpr (kEpi) {
+                    if (epi.residual && !continues)
+                        stage_residual(stage_y, epi.residual, (int64_t)acc_row0(tm, a) + 32 * q, M,
+                                       (int64_t)tn * BN + half * 128, N, lane);
+#pragma unroll 1
+                    for (int c = 0; c < 4; c++) {  // 32 columns at a time: the activation needs registers
+                        uint32_t v[32];
+                        const int64_t n = (int64_t)tn * BN + half * 128 + 32 * c + lane;
+                        const float bias = epi.bias && n < N ? half_bits_to_float(__ldcg(epi.bias + n)) : 0.f;
+                        __syncwarp();
+                        if (ok) {
+                            tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(a * 256 + half * 128 + 32 * c), v);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; i++) v[i] = 0x7fc00000u;
+                        }
+                        if (continues) {
+                            float4 *dst = slot_at(cta, a, c);
+#pragma unroll
+                            for (int i = 0; i < 8; i++)
+                                dst[32 * i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                                          __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+                            continue;
+                        }
+                        if (owner) {
+                            for (int c2 = unit + 1, s = u_end; s < tile_end; s = range_end(c2), c2++) {
+                                const float4 *src = slot_at(cta_of(c2), a, c);
+#pragma unroll
+                                for (int i = 0; i < 8; i++) {
+                                    const float4 w = __ldcg(src + 32 * i);
+                                    v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + w.x);
+                                    v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + w.y);
+                                    v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + w.z);
+                                    v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + w.w);
+                                }
+                            }
+                            if (!got)
+#pragma unroll
+                                for (int i = 0; i < 32; i++) v[i] = 0x7fc00000u;
+                        }
+                        bias_activate32(v, bias, epi.bias != nullptr, epi.act);
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            uint8_t *at = stage_y + lane * 256 + (((4 * c + j) ^ (lane & 7)) << 4);
+                            uint4 rw = make_uint4(0u, 0u, 0u, 0u);
+                            if (epi.residual) rw = *reinterpret_cast<const uint4 *>(at);
+                            uint32_t r4[4] = {rw.x, rw.y, rw.z, rw.w};
+#pragma unroll
+                            for (int e = 0; e < 4; e++) {
+                                float2 f = make_float2(__uint_as_float(v[8 * j + 2 * e]), __uint_as_float(v[8 * j + 2 * e + 1]));
+                                if (epi.residual) {
+                                    const float2 r2 = __half22float2(*reinterpret_cast<const __half2 *>(&r4[e]));
+                                    f.x += r2.x, f.y += r2.y;
+                                }
+                                const __half2 p2 = __floats2half2_rn(f.x, f.y);
+                                r4[e] = *reinterpret_cast<const uint32_t *>(&p2);
+                            }
+                            *reinterpret_cast<uint4 *>(at) = make_uint4(r4[0], r4[1], r4[2], r4[3]);
+                        }
+                    }
+                } else {
 #pragma unroll 1
                 for (int cp = 0; cp < 2; cp++) {
                     uint32_t v[64];
@@ -1006,9 +1103,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tcgen05_kernel(
 #pragma unroll
                                 for (int i = 0; i < 32; i++) vc[i] = 0x7fc00000u;
                         }
-                        if constexpr (kEpi)
-                            epilogue_row32(vc, epi, (int64_t)acc_row0(tm, a) + 32 * q + lane, M,
-                                           (int64_t)tn * BN + half * 128 + 32 * c, N);
                         // FP16 (nearest even) into the staging row of this lane
 #pragma unroll
                         for (int j = 0; j < 4; j++) {
@@ -1024,6 +1118,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tcgen05_kernel(
                         }
                     }
                 }
+                }  // kEpi
                 if (continues) continue;
                 __syncwarp();
                 // two rows of 256 bytes per instruction: lane (row parity, 16-byte chunk)
