@@ -222,10 +222,11 @@ typedef enum {
  * once.  bias: N FP16 values, or NULL for none; residual: M x N FP16, or NULL for none; act:
  * a bonsai_act.  residual may be y itself (the residual stream updated in place) but must
  * not overlap y otherwise; y must not overlap x, packed, scales or bias.  algo and split_k
- * choose the kernel as in bonsai_ternary_linear_algo (BONSAI_ALGO_AUTO and 0: the
- * automatic choice); the GEMM's CTA pairs (split_k = 3) are not available here and return
- * BONSAI_ERR_ALGO.  An unknown act returns BONSAI_ERR_ARG.  Launches the same kernels as
- * bonsai_ternary_linear_algo.  A NaN sum (that of a wait that gave up, for instance) stays a
+ * choose the kernel as in bonsai_ternary_linear_algo, except that the skinny kernel takes
+ * batches of up to 1024 tokens here (in groups of 16), which the automatic choice
+ * (BONSAI_ALGO_AUTO and 0) uses for small layers, and that the GEMM's CTA pairs
+ * (split_k = 3) are not available and return BONSAI_ERR_ALGO.  An unknown act returns
+ * BONSAI_ERR_ARG.  A NaN sum (that of a wait that gave up, for instance) stays a
  * NaN through every activation.  The pages describe no such step: the projections of a decoder
  * layer add biases and the residual stream here. */
 int bonsai_ternary_linear_epilogue(const uint16_t *x, const uint8_t *packed, const uint16_t *scales,

@@ -183,6 +183,20 @@ int resolve_algo(int algo, int64_t M, int64_t N, int64_t K, int fmt, const Devic
     }
 }
 
+// As resolve_algo, for a call with an epilogue: the skinny kernel also takes larger batches there,
+// in groups of 16 tokens that re-read the weights (from the L2, mostly), and the automatic choice
+// compares the two kernels' estimated times.  PQ2_0, us, skinny in groups against GEMM:
+//   1001 x 1024:  M = 32 11.7 / 36, M = 1024 24 / 82;  5120 x 5120: M = 64 34 / 42, M = 128 55 / 43;
+//   5120 x 17408: M = 32 47 / 58, M = 64 99 / 59.
+int resolve_epilogue_algo(int algo, int64_t M, int64_t N, int64_t K, int fmt, const DeviceInfo *dev = nullptr) {
+    if (M > 16 && skinny_groups_supported(M, N, K, fmt)) {
+        if (algo == BONSAI_ALGO_SKINNY) return algo;
+        if (algo == BONSAI_ALGO_AUTO && dev && skinny_groups_us(M, N, K, fmt) < gemm_epilogue_us(M, N, K, *dev))
+            return BONSAI_ALGO_SKINNY;
+    }
+    return resolve_algo(algo, M, N, K, fmt, dev);
+}
+
 // Launches the chosen kernel (argument checks and the workspace are the caller's).
 cudaError_t run_linear(int chosen, const uint16_t *x, const uint8_t *packed, const uint16_t *scales, uint16_t *y,
                        int64_t M, int64_t N, int64_t K, int fmt, int split_k, const Workspace &ws, cudaStream_t s,
@@ -433,7 +447,7 @@ int bonsai_ternary_linear_epilogue(const uint16_t *x, const uint8_t *packed, con
     if (!aligned16(x) || !aligned16(packed) || !aligned16(scales) || !aligned16(y) || !aligned16(bias) ||
         !aligned16(residual))
         return BONSAI_ERR_ALIGN;
-    int chosen = resolve_algo(algo, M, N, K, fmt);
+    int chosen = resolve_epilogue_algo(algo, M, N, K, fmt);
     if (chosen < 0) return chosen;
     if (algo == BONSAI_ALGO_GEMM && split_k == 3) return BONSAI_ERR_ALGO;
 
@@ -442,7 +456,7 @@ int bonsai_ternary_linear_epilogue(const uint16_t *x, const uint8_t *packed, con
     DeviceState *st;
     rc = probe_current(&dev, &st);
     if (rc != BONSAI_OK) return rc;
-    if (algo == BONSAI_ALGO_AUTO) chosen = resolve_algo(algo, M, N, K, fmt, &st->info);
+    if (algo == BONSAI_ALGO_AUTO) chosen = resolve_epilogue_algo(algo, M, N, K, fmt, &st->info);
     if (chosen == BONSAI_ALGO_IMMA && !gemv_imma_grid_fits(N, K, st->info)) return BONSAI_ERR_ALGO;
     Workspace ws;
     rc = ensure_workspace(*st, workspace_for(chosen, M, N, K, fmt, split_k, st->info),
@@ -453,7 +467,8 @@ int bonsai_ternary_linear_epilogue(const uint16_t *x, const uint8_t *packed, con
     epi.residual = residual;
     epi.act = act;
     // without any of the three the call is the plain product
-    const Epilogue *e = bias || residual || act != BONSAI_ACT_NONE ? &epi : nullptr;
+    const bool groups = chosen == BONSAI_ALGO_SKINNY && M > 16;  // only the epilogue's instance takes them
+    const Epilogue *e = bias || residual || act != BONSAI_ACT_NONE || groups ? &epi : nullptr;
     return cuda_status(run_linear(chosen, x, packed, scales, y, M, N, K, fmt, split_k, ws,
                                   static_cast<cudaStream_t>(stream), st->info, e));
 }
@@ -629,6 +644,10 @@ int bonsai_reserve(int64_t M, int64_t N, int64_t K) {
             }
         if (skinny_supported(M < 16 ? M : 16, N, K, fmt)) {
             v = skinny_workspace_bytes(M < 16 ? M : 16, N, K, fmt, 0, st->info);
+            need = v > need ? v : need;
+        }
+        if (M > 16 && skinny_groups_supported(M < kSkinnyMaxTokens ? M : kSkinnyMaxTokens, N, K, fmt)) {
+            v = skinny_workspace_bytes(M < kSkinnyMaxTokens ? M : kSkinnyMaxTokens, N, K, fmt, 0, st->info);
             need = v > need ? v : need;
         }
         if (gemm_supported(M, N, K, fmt)) {

@@ -35,6 +35,8 @@
 // hands NaN over for a split one), and sets its bit in the device status word.
 #include <cuda.h>
 
+#include <cmath>
+
 #include "common.cuh"
 #include "internal.h"
 #include "tma.cuh"
@@ -1216,11 +1218,29 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int tile_hint, int sm_count)
     return p;
 }
 
+// Calls with an epilogue split a tile's K stages over fewer CTAs when there are few tiles: a
+// stage costs about 0.55 us per accumulator, a further piece about 2 us (its 128 KB of sums go
+// through the L2 to the tile's owner), so p pieces of nk stages take 0.55 nk / p + 2 p, least at
+// p = sqrt(0.275 nk).
+int64_t epilogue_ctas(const GemmPlan &p) {
+    int64_t pieces = (int64_t)(std::sqrt(0.275 * (double)p.nk) + 0.5);
+    pieces = pieces < 1 ? 1 : pieces;
+    const int64_t c = (int64_t)p.mt * p.nt * pieces;
+    return c < p.ctas ? c : p.ctas;
+}
+
 constexpr size_t kSlotBytes = (size_t)2 * BM * BN * 4;  // one CTA's FP32 partial tile (two accumulators)
 
 size_t x_rot_bytes(int64_t M, int64_t K) { return (((size_t)M * (size_t)K * 2) + 255) / 256 * 256; }
 
 }  // namespace
+
+double gemm_epilogue_us(int64_t M, int64_t N, int64_t K, const DeviceInfo &dev) {
+    const GemmPlan p = gemm_plan(M, N, K, 0, dev.sm_count);
+    const double ctas = (double)epilogue_ctas(p), tiles = (double)p.mt * p.nt;
+    const double pieces = ctas > tiles ? ctas / tiles : 1.0;
+    return 22.0 + p.acc * (2.0 * pieces + 0.55 * (double)p.units / ctas);
+}
 
 bool gemm_supported(int64_t M, int64_t N, int64_t K, int fmt) {
     if (fmt < 1 || fmt > 4) return false;
@@ -1247,6 +1267,7 @@ cudaError_t launch_gemm(const uint16_t *x, const uint8_t *packed, const uint16_t
     const Epilogue ep = epi ? *epi : Epilogue{};
     if (swiglu && N != 2 * swiglu_f) return cudaErrorInvalidValue;
     GemmPlan plan = gemm_plan(M, N, K, tile_hint, dev.sm_count);
+    if (epi) plan.ctas = (int)epilogue_ctas(plan);
     if (ws.data_bytes < gemm_workspace_bytes(M, N, K, fmt, dev) || plan.ctas > kCtlGemmMaxCtas ||
         ws.zeroed_bytes < kCtlRegionBytes)
         return cudaErrorInvalidValue;

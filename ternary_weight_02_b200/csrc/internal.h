@@ -105,6 +105,10 @@ cudaError_t launch_gemv_imma(const uint16_t *x, const uint8_t *packed, const uin
 // ---- skinny_mma.cu: 1 <= M <= 16 (one launch when its grid is resident at once: the
 // rotation, a barrier on the call counter in Workspace::zeroed, the kernel; else two)
 bool skinny_supported(int64_t M, int64_t N, int64_t K, int fmt);
+// epilogue calls: larger batches in groups of 16 tokens, one grid slice each
+constexpr int64_t kSkinnyMaxTokens = 1024;
+bool skinny_groups_supported(int64_t M, int64_t N, int64_t K, int fmt);
+double skinny_groups_us(int64_t M, int64_t N, int64_t K, int fmt);  // estimate, for the automatic choice
 size_t skinny_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, int split_k,
                               const DeviceInfo &dev);
 int skinny_launches(int64_t M, int64_t N, int64_t K, int fmt, int split_k, const DeviceInfo &dev);
@@ -118,6 +122,7 @@ cudaError_t launch_swiglu(const uint16_t *y, uint16_t *h, int64_t M, int64_t F, 
 
 // ---- gemm_tcgen05.cu: prefill
 bool gemm_supported(int64_t M, int64_t N, int64_t K, int fmt);
+double gemm_epilogue_us(int64_t M, int64_t N, int64_t K, const DeviceInfo &dev);  // estimate of a call with an epilogue
 size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, const DeviceInfo &dev);
 // tile_hint: 0 automatic, 1 one 128-row accumulator per CTA, 2 two (256 rows).  One launch:
 // the rotation of x into the workspace, a grid barrier, the tiles; hand-over flags and the

@@ -47,6 +47,11 @@
 //   codes and the lane assembles the same two code words (weights 32tq .. 32tq + 31) the
 //   PQ2_0 path loads; everything after that is PQ2_0's.  The lane's 7 or 8 bytes of a row's
 //   group (from byte 32tq / 5) come as three aligned 32-bit loads.
+// * Calls with an epilogue (kEpi: bias, activation, residual on the FP32 sums) take larger
+//   batches too, as grid slices of 16 tokens that re-read the weights through the L2: the
+//   batch-independent cost of the GEMM (rotation, grid barrier, hand-over of split tiles: 25
+//   to 80 us) is more than that for small layers.  1001 x 1024, PQ2_0, M = 100: 12 us
+//   against 39; the choice is made by the two kernels' estimated times.
 #include <cstring>
 
 #include "common.cuh"
@@ -60,6 +65,16 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRowsPerCta = kWarps * 16;
 constexpr int kRing = 8;  // groups of weights in flight per warp (register ring)
+
+// Larger batches go in groups of kTokens tokens, one grid slice each (epilogue calls only):
+// a group's part of the workspace, its staged x' and its group sums.
+constexpr int kTokens = 16;
+__host__ __device__ constexpr size_t staged_group_bytes(int64_t K) {
+    return ((size_t)(K / kGroup) * 8 * kTokens * 32 + 255) / 256 * 256;
+}
+__host__ __device__ constexpr size_t gsum_group_bytes(int64_t K) {  // room for the g64 half sums
+    return ((size_t)(K / kGroup) * 2 * kTokens * 4 + 255) / 256 * 256;
+}
 
 // groups of x' staged in shared memory at a time: 96 KB for either token tile count
 template <int NT>
@@ -189,6 +204,11 @@ __global__ void __launch_bounds__(256) skinny_prep_kernel(const uint16_t *__rest
                                                           float *__restrict__ gsum, int M, int64_t K) {
     const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     if (w >= (K / kGroup) * MT) return;
+    if (blockIdx.y > 0) {  // a later group of tokens
+        x += (int64_t)blockIdx.y * kTokens * K, M -= (int)blockIdx.y * kTokens;
+        xs += blockIdx.y * (staged_group_bytes(K) / sizeof(uint16_t)), gsum += blockIdx.y * (gsum_group_bytes(K) / sizeof(float));
+    }
+    if (M > kTokens) M = kTokens;
     prep_task<MT, kFmt>(x, xs, gsum, M, K, w, threadIdx.x & 31);
 }
 
@@ -237,6 +257,20 @@ __global__ void __launch_bounds__(kThreads) skinny_kernel(
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gid = lane >> 2, tq = lane & 3;
     const int64_t G = K / kGroup;
+    if constexpr (kEpi) {  // this grid slice's group of tokens
+        const int64_t z = blockIdx.z;
+        if (z > 0) {
+            M -= (int)z * kTokens;
+            xsg += z * (staged_group_bytes(K) / sizeof(uint16_t));
+            gsg += z * (gsum_group_bytes(K) / sizeof(float));
+            y += z * kTokens * N;
+            if (epi.residual) epi.residual += z * kTokens * N;
+            if (x) x += z * kTokens * K;
+            partials += z * S * kTokens * N;
+            counters += z * ((N + 15) / 16);
+        }
+        if (M > kTokens) M = kTokens;
+    }
     const int chunk = blockIdx.y;
     const int g_begin = chunk * gpc;
     const int g_end = (int)((int64_t)(chunk + 1) * gpc < G ? (int64_t)(chunk + 1) * gpc : G);
@@ -253,9 +287,9 @@ __global__ void __launch_bounds__(kThreads) skinny_kernel(
     // ---- the rotation phase and this CTA's arrival (fused launch)
     unsigned long long arrival = 0;
     if (x != nullptr) {
-        const int64_t ncta = (int64_t)gridDim.x * gridDim.y;
+        const int64_t slice = (int64_t)gridDim.x * gridDim.y, ncta = kEpi ? slice * gridDim.z : slice;
         const int64_t b = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
-        for (int64_t w = b * kWarps + warp; w < G * MT; w += ncta * kWarps)
+        for (int64_t w = b * kWarps + warp; w < G * MT; w += slice * kWarps)
             prep_task<MT, kFmt>(x, xsg, gsg, M, K, w, lane);
         __threadfence();
         __syncthreads();
@@ -607,12 +641,14 @@ int smem_bytes(int NT, int gpc, int fmt, bool tma) {
     return 1024 + kWarps * kTStages * (ws + ss) + xs + ((gs + 7) & ~7) + kWarps * kTStages * 8;
 }
 
+int64_t token_groups(int64_t M) { return (M + kTokens - 1) / kTokens; }
+
 // K chunks: about as many CTAs as fit on the GPU at once (one wave; a CTA's registers
 // allow two per SM), unless split_k (> 0) says otherwise.  With the TMA ring a chunk is
 // a whole number of stages (kTGroups groups).
-void choose_split(int64_t N, int64_t K, int split_k, bool tma, const DeviceInfo &dev, int *S, int *gpc) {
+void choose_split(int64_t M, int64_t N, int64_t K, int split_k, bool tma, const DeviceInfo &dev, int *S, int *gpc) {
     const int64_t G = K / kGroup;
-    const int64_t rb = (N + kRowsPerCta - 1) / kRowsPerCta;
+    const int64_t rb = (N + kRowsPerCta - 1) / kRowsPerCta * token_groups(M);
     int64_t s = split_k > 0 ? split_k : (2 * (int64_t)dev.sm_count) / rb;
     if (s < 1) s = 1;
     if (s > G) s = G;
@@ -625,10 +661,12 @@ void choose_split(int64_t N, int64_t K, int split_k, bool tma, const DeviceInfo 
 // Workspace: the staged x' ([G][8][MT][16] FP16), the group sums ([G][MT] FP32; g64
 // [G][2][MT]), then the split-K partials.
 size_t staged_bytes(int64_t M, int64_t K) {
+    if (M > kTokens) return (size_t)token_groups(M) * staged_group_bytes(K);
     const int64_t MT = M <= 8 ? 8 : 16;
     return ((size_t)(K / kGroup) * 8 * MT * 32 + 255) / 256 * 256;
 }
 size_t gsum_bytes(int64_t M, int64_t K) {  // room for the g64 half sums
+    if (M > kTokens) return (size_t)token_groups(M) * gsum_group_bytes(K);
     const int64_t MT = M <= 8 ? 8 : 16;
     return ((size_t)(K / kGroup) * 2 * MT * 4 + 255) / 256 * 256;
 }
@@ -663,8 +701,8 @@ template <bool kEpi>
 cudaError_t grid_fits(int64_t M, int64_t N, int64_t K, int fmt, int split_k, const DeviceInfo &dev, bool *fits) {
     const bool tma = use_tma(K, fmt);
     int S, gpc;
-    choose_split(N, K, split_k, tma, dev, &S, &gpc);
-    const int64_t ctas = ((N + kRowsPerCta - 1) / kRowsPerCta) * S;
+    choose_split(M, N, K, split_k, tma, dev, &S, &gpc);
+    const int64_t ctas = ((N + kRowsPerCta - 1) / kRowsPerCta) * S * token_groups(M);
     const int NT = M <= 8 ? 1 : 2;
     const int smem = smem_bytes(NT, gpc, fmt, tma);
     return NT == 1 ? kernel_fits_fmt<1, kEpi>(fmt, tma, ctas, smem, dev, fits)
@@ -673,6 +711,16 @@ cudaError_t grid_fits(int64_t M, int64_t N, int64_t K, int fmt, int split_k, con
 
 }  // namespace
 
+double skinny_groups_us(int64_t M, int64_t N, int64_t K, int fmt) {
+    const double per = fmt == 1 ? 0.34 : fmt == 3 ? 0.15 : fmt == 4 ? 0.22 : 0.20;  // us per 10^6 weights of a group
+    return 14.0 + per * 1e-6 * (double)token_groups(M) * (double)N * (double)K;
+}
+
+bool skinny_groups_supported(int64_t M, int64_t N, int64_t K, int fmt) {
+    return skinny_supported(M < kTokens ? M : kTokens, N, K, fmt) && M <= kSkinnyMaxTokens &&
+           token_groups(M) * ((N + 15) / 16) <= kMaxTiles;
+}
+
 bool skinny_supported(int64_t M, int64_t N, int64_t K, int fmt) {
     return fmt >= 1 && fmt <= 4 && M >= 1 && M <= 16 && K % kGroup == 0 && (N + 15) / 16 <= kMaxTiles &&
            K < ((int64_t)1 << 31);
@@ -680,8 +728,8 @@ bool skinny_supported(int64_t M, int64_t N, int64_t K, int fmt) {
 
 size_t skinny_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, int split_k, const DeviceInfo &dev) {
     int S, gpc;
-    choose_split(N, K, split_k, use_tma(K, fmt), dev, &S, &gpc);
-    return staged_bytes(M, K) + gsum_bytes(M, K) + (S > 1 ? (size_t)S * (size_t)M * (size_t)N * sizeof(float) : 0);
+    choose_split(M, N, K, split_k, use_tma(K, fmt), dev, &S, &gpc);
+    return staged_bytes(M, K) + gsum_bytes(M, K) + (S > 1 ? (size_t)S * (size_t)(M > kTokens ? token_groups(M) * kTokens : M) * (size_t)N * sizeof(float) : 0);
 }
 
 int skinny_launches(int64_t M, int64_t N, int64_t K, int fmt, int split_k, const DeviceInfo &dev) {
@@ -701,8 +749,9 @@ cudaError_t launch(const uint16_t *x, const uint8_t *packed, const uint16_t *sca
     float *partials = reinterpret_cast<float *>(ws.data + staged_bytes(M, K) + gsum_bytes(M, K));
     const bool tma = use_tma(K, fmt);
     int S, gpc;
-    choose_split(N, K, split_k, tma, dev, &S, &gpc);
-    const dim3 grid((unsigned)((N + kRowsPerCta - 1) / kRowsPerCta), (unsigned)S);
+    choose_split(M, N, K, split_k, tma, dev, &S, &gpc);
+    if (M > kTokens && !kEpi) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)((N + kRowsPerCta - 1) / kRowsPerCta), (unsigned)S, (unsigned)token_groups(M));
     const int64_t G = K / kGroup;
     // tensor maps of the packed plane (rows of G x 32 bytes, Q1_0 16; boxes of 128 bytes x
     // 16 rows, 128-byte swizzle) and of the scale plane (rows of G or 2G FP16; boxes of 8
@@ -737,7 +786,8 @@ cudaError_t launch(const uint16_t *x, const uint8_t *packed, const uint16_t *sca
         const int smem = smem_bytes(NT, gpc, fmt, tma);
         cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (err != cudaSuccess) return err;
-        if (!fused) prep<<<(unsigned)((G * MT + 7) / 8), 256, 0, s>>>(x, xsg, gsg, (int)M, K);
+        if (!fused)
+            prep<<<dim3((unsigned)((G * MT + 7) / 8), (unsigned)token_groups(M)), 256, 0, s>>>(x, xsg, gsg, (int)M, K);
         kern<<<grid, kThreads, smem, s>>>(xsg, gsg, packed, scales, y, partials, ws.counters, (int)M, N, K, S, gpc,
                                           fused ? x : nullptr, reinterpret_cast<unsigned int *>(ws.zeroed), wmap,
                                           smap, epi);
