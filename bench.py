@@ -16,6 +16,9 @@ CUDA graph.
   e2e        the same metric through the C ABI with pinned host buffers: every step
              copies the step's activations host -> device and its outputs back.
   cpu_baseline  the float64 CPU checker on a bounded sample (one layer), rank 0, N=1.
+  decode_layers  with --context L: one token through 64 whole decoder layers at a context of
+             L positions (qkv with bias, rotary positions and cache append, attention over the
+             paged cache, o with the residual, gate/up with SwiGLU, down with the residual).
 
 Multi-GPU: one process per GPU (torchrun); each rank decodes its own token stream
 through its own copy of the stack (replicas, weak scaling, no collective on the
@@ -403,6 +406,8 @@ def measure_decode(f, base, dev, bz, torch, args, world, hbm):
            "per_projection": per, "e2e": e2e, "h2d": h2d, "d2h": d2h, "traffic": kernel_traffic(f)}
     if f == 2:
         out["swiglu_decode"] = measure_swiglu_decode(stack, xs, bz, torch, stream, dev, args)
+    if args.context > 0 and f == FMTS[args.fmt]:
+        out["decode_layers"] = measure_decode_layers(f, stack, bz, torch, stream, dev, args, hbm)
     if args.skinny and f in (1, 2):
         out["skinny_grid"] = measure_skinny_grid(f, stack, dev, bz, torch, stream, args, hbm)
     del stack, g
@@ -517,6 +522,8 @@ def run_ours(args):
         grids = {FMT_NAMES[k]: v["skinny_grid"] for k, v in results.items() if "skinny_grid" in v}
         if grids:
             line["skinny"] = grids
+        if "decode_layers" in r:
+            line["decode_layers"] = r["decode_layers"]
         sw = next((v["swiglu_decode"] for v in results.values() if "swiglu_decode" in v), None)
         if sw is not None:
             line["swiglu"] = {"decode": sw}
@@ -558,6 +565,57 @@ def measure_swiglu_decode(stack, xs, bz, torch, stream, dev, args):
 
 
 PREFILL_MS = (512, 2048, 8192)  # the prefill workload's token counts
+
+
+def measure_decode_layers(f, stack, bz, torch, stream, dev, args, hbm):
+    """One token through LAYERS decoder layers at a context of args.context positions: the
+    stack's projections with what lies between them (40 query and 8 key/value heads of 128,
+    the 7168 rows of qkv), each layer with its own FP16 cache in pages of 64.  Times the whole
+    step and the attention calls alone; bytes are the projections' and the cache's."""
+    Hq, Hkv, D, page = 40, 8, 128, 64
+    d, F, L = Hq * D, SHAPES[2][2] // 2, args.context
+    width = (L + page - 1) // page
+    gen = torch.Generator(device=dev).manual_seed(0)
+    pools = [[torch.randn((width, Hkv, page, D), generator=gen, device=dev, dtype=torch.float16) for _ in range(2)]
+             for _ in range(LAYERS)]
+    table = torch.randperm(width, generator=gen, device=dev).to(torch.int32).view(1, width)
+    lengths = torch.tensor([L], dtype=torch.int32, device=dev)
+    positions = lengths - 1
+    slots = (table[0, (L - 1) // page].long() * page + (L - 1) % page).view(1)
+    freqs, mag = bz.bonsai_rope_frequencies(D, 1e6)
+    freqs = freqs.to(dev)
+    f16 = dict(dtype=torch.float16, device=dev)
+    x, bias = torch.randn((1, d), generator=gen, **f16), torch.randn(SHAPES[0][2], generator=gen, **f16)
+    qkv, q, att, h = (torch.empty((1, n), **f16) for n in (SHAPES[0][2], d, d, F))
+    sp = stream.cuda_stream
+
+    def attend(layer):
+        bz.bonsai_paged_attention(q, *pools[layer], None, None, table, lengths, att, 1, Hq, stream=sp)
+
+    def step():
+        for layer in range(LAYERS):
+            (wq, sq), (wo, so), (wg, sg), (wd, sd) = (stack[i][layer] for i in range(4))
+            bz.bonsai_ternary_linear_epilogue(x, wq, sq, bias, None, qkv, 1, SHAPES[0][2], d, f, stream=sp)
+            bz.bonsai_rope_append(qkv, q, *pools[layer], None, None, freqs, positions, slots, 1, Hq, D, magnitude=mag,
+                                  stream=sp)
+            attend(layer)
+            bz.bonsai_ternary_linear_epilogue(att, wo, so, None, x, x, 1, d, d, f, stream=sp)
+            bz.bonsai_ternary_linear_swiglu(x, wg, sg, h, 1, F, d, f, sp)
+            bz.bonsai_ternary_linear_epilogue(h, wd, sd, None, x, x, 1, d, F, f, stream=sp)
+
+    def attention_only():
+        for layer in range(LAYERS):
+            attend(layer)
+
+    out = {}
+    cache = LAYERS * 2 * 2 * L * Hkv * D
+    for name, fn, nbytes in (("step", step, step_bytes(f) + cache), ("attention", attention_only, cache)):
+        g = capture(torch, stream, fn)
+        us = time_graph(torch, stream, g, max(3, min(args.steps, 20))) * 1e3
+        out[name] = {"us": round(us, 2), "us_per_layer": round(us / LAYERS, 3), "gbs": round(nbytes / us / 1e3, 1),
+                     "frac": round(nbytes / us / 1e3 / hbm, 4)}
+        del g
+    return {"context": L, "packing": FMT_NAMES[f], "heads": [Hq, Hkv, D], **out}
 
 
 def measure_prefill(fmt, base, dev, bz, torch, args, peaks, peak_kind):
@@ -729,6 +787,8 @@ def main():
     ap.add_argument("--prefill-ms", default=",".join(str(m) for m in PREFILL_MS),
                     help="token counts of the prefill grid (comma-separated)")
     ap.add_argument("--skinny", type=int, default=1, help="measure the M = 1..16 decode grid (PQ2_0, PTQ1_0)")
+    ap.add_argument("--context", type=int, default=0,
+                    help="also measure whole decoder layers at this context length (0: no)")
     ap.add_argument("--case", choices=["gemv", "imma", "gemm", "skinny"], help="run one projection only (profiler case)")
     ap.add_argument("--shape", choices=[n for n, _, _ in SHAPES], default="gate_up")
     ap.add_argument("--m", type=int, default=2048,
