@@ -109,6 +109,13 @@ for _name, (_res, _args) in _SIGS.items():
     _fn.argtypes = _args
 
 
+try:
+    from . import _bonsai_call as _call  # the per-layer entry points without ctypes' conversions
+except ImportError as e:
+    raise ImportError("_bonsai_call.so is missing or does not load; build it with "
+                      "`python -m ternary_weight_02_b200.build`") from e
+
+
 class BonsaiError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -139,6 +146,14 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _stream_on(stream, dev: int):
+    """_stream() where the current device's index is known."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
 
 
 def _check(rc: int, where: str) -> int:
@@ -188,7 +203,7 @@ def bonsai_hadamard128(x, x_out, M: int, K: int, stream=None) -> None:
 
 def bonsai_ternary_linear(x, packed, scales, y, M: int, N: int, K: int, fmt: int,
                           stream=None) -> None:
-    _check(_lib.bonsai_ternary_linear(_ptr(x), _ptr(packed), _ptr(scales), _ptr(y), M, N, K, fmt,
+    _check(_call.bonsai_ternary_linear(_ptr(x), _ptr(packed), _ptr(scales), _ptr(y), M, N, K, fmt,
                                       _stream(stream)), "bonsai_ternary_linear")
 
 
@@ -242,7 +257,7 @@ def bonsai_swiglu(y, h, M: int, F: int, stream=None) -> None:
 
 
 def bonsai_ternary_linear_swiglu(x, packed, scales, h, M: int, F: int, K: int, fmt: int, stream=None) -> None:
-    _check(_lib.bonsai_ternary_linear_swiglu(_ptr(x), _ptr(packed), _ptr(scales), _ptr(h), M, F, K, fmt,
+    _check(_call.bonsai_ternary_linear_swiglu(_ptr(x), _ptr(packed), _ptr(scales), _ptr(h), M, F, K, fmt,
                                              _stream(stream)), "bonsai_ternary_linear_swiglu")
 
 
@@ -297,9 +312,9 @@ def bonsai_ternary_linear_epilogue(x, packed, scales, bias, residual, y, M: int,
     """y = act(x' . Wdeq^T + bias) + residual; bias and residual may be None, residual may be y."""
     import torch
     dev, f16 = torch.cuda.current_device(), torch.float16
-    _check(_lib.bonsai_ternary_linear_epilogue(
+    _check(_call.bonsai_ternary_linear_epilogue(
         _dev(x, f16, M * K, dev), _dev(packed, torch.uint8, 0, dev), _dev(scales, f16, 0, dev), _dev(bias, f16, N, dev),
-        _dev(residual, f16, M * N, dev), _dev(y, f16, M * N, dev), M, N, K, fmt, act, algo, split_k, _stream(stream)),
+        _dev(residual, f16, M * N, dev), _dev(y, f16, M * N, dev), M, N, K, fmt, act, algo, split_k, _stream_on(stream, dev)),
         "bonsai_ternary_linear_epilogue")
 
 
@@ -322,19 +337,19 @@ def bonsai_rope(x, out, freqs, positions, T: int, H: int, D: int, R: int, layout
     dev = torch.cuda.current_device()
     xp, ld_x = _rows(x, T, H * D, ld_x, dev)
     op, ld_out = _rows(out, T, H * D, ld_out, dev)
-    _check(_lib.bonsai_rope(xp, op, _dev(freqs, torch.float64, R // 2, dev), _dev(positions, torch.int32, T, dev), T, H, D,
-                            R, ld_x, ld_out, magnitude, layout, _stream(stream)), "bonsai_rope")
+    _check(_call.bonsai_rope(xp, op, _dev(freqs, torch.float64, R // 2, dev), _dev(positions, torch.int32, T, dev), T, H, D,
+                            R, ld_x, ld_out, magnitude, layout, _stream_on(stream, dev)), "bonsai_rope")
 
 
 def _pools(k_cache, v_cache, k_scale, v_scale, dev: int):
     """Pointers of a pair of cache pools and their scales, and (pages, Hkv, page_size, D, kv_type)."""
     import torch
-    kind = k_cache.dtype
+    kind, shape = k_cache.dtype, k_cache.shape
     if kind is not torch.float16 and kind is not torch.float8_e4m3fn:
         raise ValueError("a cache holds float16 or float8_e4m3fn values")
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache are two pools of the same shape: pages x Hkv x page_size x D")
-    pages, Hkv, page_size, D = k_cache.shape
+    pages, Hkv, page_size, D = shape
     f32 = torch.float32
     return ((_dev(k_cache, kind, 0, dev), _dev(v_cache, kind, 0, dev), _dev(k_scale, f32, Hkv, dev),
              _dev(v_scale, f32, Hkv, dev)),
@@ -351,9 +366,9 @@ def bonsai_rope_append(qkv, q_out, k_cache, v_cache, k_scale, v_scale, freqs, po
     ptrs, (pages, Hkv, page_size, D, kind) = _pools(k_cache, v_cache, k_scale, v_scale, dev)
     xp, ld_qkv = _rows(qkv, T, (Hq + 2 * Hkv) * D, ld_qkv, dev)
     qp, ld_q = _rows(q_out, T, Hq * D, ld_q, dev)
-    _check(_lib.bonsai_rope_append(xp, qp, *ptrs, _dev(freqs, torch.float64, R // 2, dev),
+    _check(_call.bonsai_rope_append(xp, qp, *ptrs, _dev(freqs, torch.float64, R // 2, dev),
                                    _dev(positions, torch.int32, T, dev), _dev(slots, torch.int64, T, dev), T, Hq, Hkv, D,
-                                   R, ld_qkv, ld_q, pages, page_size, magnitude, layout, kind, _stream(stream)),
+                                   R, ld_qkv, ld_q, pages, page_size, magnitude, layout, kind, _stream_on(stream, dev)),
            "bonsai_rope_append")
 
 
@@ -367,10 +382,10 @@ def bonsai_paged_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, le
     qp, ld_q = _rows(q, B, Hq * D, ld_q, dev)
     op, ld_out = _rows(out, B, Hq * D, ld_out, dev)
     width = page_table.shape[-1]
-    _check(_lib.bonsai_paged_attention(qp, *ptrs, _dev(page_table, i32, B * width, dev), _dev(lengths, i32, B, dev), op,
+    _check(_call.bonsai_paged_attention(qp, *ptrs, _dev(page_table, i32, B * width, dev), _dev(lengths, i32, B, dev), op,
                                        _dev(lse, torch.float32, B * Hq, dev), B, Hq, Hkv, D, ld_q, ld_out, pages,
                                        page_size, width, window, D ** -0.5 if scale is None else scale, kind,
-                                       _stream(stream)), "bonsai_paged_attention")
+                                       _stream_on(stream, dev)), "bonsai_paged_attention")
 
 
 def pack(fmt: int, trits, stream=None):

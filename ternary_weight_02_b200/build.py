@@ -4,7 +4,8 @@
 
 Each csrc/*.cu is compiled to an object under _build/ (in parallel, skipped when
 up to date) and linked with the static CUDA runtime into
-ternary_weight_02_b200/libbonsai.so.  Only nvcc is needed; no GPU.
+ternary_weight_02_b200/libbonsai.so.  csrc/pycall.c, the binding's fast call path, becomes
+the extension module _bonsai_call.so beside it (gcc and the Python headers).  No GPU needed.
 """
 from __future__ import annotations
 
@@ -14,12 +15,15 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbonsai.so")
+CALL_SRC = os.path.join(CSRC, "pycall.c")
+CALL = os.path.join(PKG, "_bonsai_call.so")
 HEADER = os.path.join(ROOT, "include", "bonsai.h")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -69,6 +73,15 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
         os.replace(tmp, LIB)
+    if (force or not os.path.exists(CALL)
+            or os.path.getmtime(CALL) < max(os.path.getmtime(CALL_SRC), os.path.getmtime(HEADER))):
+        tmp = CALL + ".tmp"
+        cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], CALL_SRC,
+               "-o", tmp, "-L", PKG, "-l:libbonsai.so", "-Wl,-rpath,$ORIGIN"]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"building {os.path.basename(CALL)} failed:\n{res.stdout}\n{res.stderr}")
+        os.replace(tmp, CALL)
     return LIB
 
 
