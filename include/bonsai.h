@@ -282,8 +282,8 @@ int bonsai_rope(const uint16_t *x, uint16_t *out, const double *freqs, const int
 /* Element types of a paged key/value cache. */
 typedef enum {
     BONSAI_KV_F16 = 0, /* FP16                                                             */
-    BONSAI_KV_E4M3 = 1 /* 8-bit floats (4 exponent, 3 mantissa bits) times an FP32 scale per
-                          key/value head: k_scale and v_scale, Hkv values each              */
+    BONSAI_KV_E4M3 = 1 /* 8-bit floats (4 exponent, 3 mantissa bits) times a positive FP32
+                          scale per key/value head: k_scale and v_scale, Hkv values each    */
 } bonsai_kv_type;
 
 /* A paged key/value cache is two pools, k_cache and v_cache, of `pages` pages each:
@@ -321,7 +321,8 @@ int bonsai_rope_append(const uint16_t *qkv, uint16_t *q_out, void *k_cache, void
  * rows of Hq heads of D FP16 elements at row strides ld_q and ld_out; out must not overlap
  * q or the cache.  lse (may be NULL) gets the B x Hq FP32 natural logarithms of the sums of
  * e^(scale q.k), so that results over parts of a context can be joined.  A sequence of
- * length 0 gives zeros and an lse of -infinity.
+ * length 0 gives zeros and an lse of -infinity; one whose scores are all -infinity gives
+ * NaN, as the formula does.
  *   page_table: B rows of max_pages int32 page numbers; entries past a sequence's last page
  * (and before its window) are not read.  lengths: B int32 values.  Entries of the cache at
  * other positions (the rest of the last page, freed pages) are never part of a result,

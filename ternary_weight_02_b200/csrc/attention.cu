@@ -614,7 +614,9 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const __grid_consta
             const int i = j * kWarps + warp, qi = nt * 8 + 2 * tig;
             const int d = kType == 0 ? 16 * i + gid : 16 * i + 2 * gid, step = kType == 0 ? 8 : 1;
             uint16_t *at = p.out + (int64_t)b * p.ld_out + (head0 + qi) * D + d;
-            const float i0 = lt.x == 0.f ? 0.f : vs / lt.x, i1 = lt.y == 0.f ? 0.f : vs / lt.y;
+            // no keys: 0; keys whose scores are all -infinity have a sum of 0 too, and give 0 / 0
+            const bool none = s.len == s.first && !s.bad;
+            const float i0 = none ? 0.f : vs / lt.x, i1 = none ? 0.f : vs / lt.y;
             if (qi < nq) at[0] = float_to_half_bits(v.x * i0), at[step] = float_to_half_bits(v.z * i0);
             if (qi + 1 < nq) at[D] = float_to_half_bits(v.y * i1), at[D + step] = float_to_half_bits(v.w * i1);
         };

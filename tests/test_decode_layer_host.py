@@ -99,6 +99,7 @@ def test_rope_refusals(bz):
     for kw in ({"T": -1}, {"H": -1}, {"D": 0}, {"D": 60}, {"D": 2048}, {"R": 3}, {"R": -2}, {"R": 66}, {"ld_x": 120},
                {"ld_out": 120}, {"ld_x": 129}, {"ld_out": 132}):
         assert call(**kw) == bz.BONSAI_ERR_SHAPE, kw
+    assert call(ld_x=256) == bz.BONSAI_ERR_SHAPE  # x is out here: in place, the rows are the same
     assert call(T=0, x=None) == bz.BONSAI_OK
     assert call(H=0, ld_x=0, ld_out=0, x=None) == bz.BONSAI_OK
 
@@ -108,7 +109,7 @@ CACHE_SHAPES = [{"Hkv": 0}, {"Hkv": 3}, {"Hkv": -2}, {"D": 96}, {"D": 512}, {"pa
 
 
 def test_append_refusals(bz):
-    def call(qkv=GOOD, q_out=GOOD, k=GOOD, v=GOOD, ks=GOOD, vs=GOOD, freqs=GOOD, positions=GOOD, slots=GOOD, T=4, Hq=4,
+    def call(qkv=GOOD, q_out=2 * GOOD, k=GOOD, v=GOOD, ks=GOOD, vs=GOOD, freqs=GOOD, positions=GOOD, slots=GOOD, T=4, Hq=4,
              Hkv=2, D=64, R=64, ld_qkv=512, ld_q=256, pages=8, page_size=16, layout=0, kv_type=1):
         return bz.raw().bonsai_rope_append(qkv, q_out, k, v, ks, vs, freqs, positions, slots, T, Hq, Hkv, D, R, ld_qkv,
                                            ld_q, pages, page_size, 1.0, layout, kv_type, None)
@@ -120,6 +121,7 @@ def test_append_refusals(bz):
     assert call(layout=2) == call(kv_type=2) == call(kv_type=-1) == bz.BONSAI_ERR_ARG
     for kw in CACHE_SHAPES + [{"T": -1}, {"R": 66}, {"R": 5}, {"ld_qkv": 504}, {"ld_q": 248}, {"ld_q": 257}]:
         assert call(**kw) == bz.BONSAI_ERR_SHAPE, kw
+    assert call(q_out=GOOD) == bz.BONSAI_ERR_SHAPE  # in place, but with another row stride
     assert call(T=0, qkv=None) == bz.BONSAI_OK
 
 

@@ -213,3 +213,25 @@ def test_attention_large_batch(bz):
     q = rng.normal(0, 2, (len(lengths), Hq, D)).astype(np.float16)
     got, lse = run(bz, q, pool.device(), Hq)
     check(got, lse, q, pool, 0, D ** -0.5)
+
+
+def test_attention_scores_of_minus_infinity(bz):
+    """Keys of -infinity among others have no weight; where there is nothing else the result is the
+    formula's NaN, with an lse of -infinity; the other heads and sequences are untouched."""
+    rng = np.random.default_rng(15)
+    lengths, Hq, Hkv, D, page = [40, 40, 200], 4, 2, 64, 16
+    pool = ref.Pool(rng, lengths, Hkv, D, page, 0)
+    q = np.abs(rng.normal(0, 2, (3, Hq, D))).astype(np.float16) + np.float16(0.1)
+    for b, keys in ((0, range(40)), (1, range(0, 40, 3)), (2, range(200))):
+        for j in keys:  # head 0's keys
+            pool.kbits[pool.table[b, j // page], 0, j % page] = 0xfc00
+            pool.k[b][j, 0] = -np.inf
+    got, lse = run(bz, q, pool.device(), Hq)
+    for b in (0, 2):
+        assert np.isnan(got[b, :2]).all() and np.isneginf(lse[b, :2]).all()
+        assert np.isfinite(got[b, 2:]).all() and np.isfinite(lse[b, 2:]).all()
+    keep = np.array([j for j in range(40) if j % 3])
+    want, want_lse, tol, lse_tol = ref.attention(q[1:2].astype(np.float64), [pool.k[1][keep]], [pool.v[1][keep]], [len(keep)], 0,
+                                                 D ** -0.5)
+    assert (np.abs(got[1:2, :2] - want[:, :2]) <= tol[:, :2]).all()
+    assert (np.abs(lse[1:2, :2] - want_lse[:, :2]) <= lse_tol[:, :2]).all()
