@@ -59,12 +59,22 @@ __device__ __forceinline__ float activate(float z, int act) {
     }
 }
 
-// Read through L2: the residual may be the output buffer, which the kernel also writes.
-__device__ __forceinline__ float epilogue_value(float v, const Epilogue &e, int64_t m, int64_t n, int64_t N) {
-    if (e.bias) v += half_bits_to_float(__ldcg(e.bias + n));
+// Bias and residual of one output, read ahead of its sum (a load behind the store of another
+// output would wait for it: the residual may be the output buffer, so the two are not
+// reordered; through the L2 for the same reason).
+struct EpilogueTerms {
+    float bias = 0.f, residual = 0.f;
+};
+__device__ __forceinline__ EpilogueTerms epilogue_terms(const Epilogue &e, int64_t m, int64_t n, int64_t N) {
+    EpilogueTerms t;
+    if (e.bias) t.bias = half_bits_to_float(__ldcg(e.bias + n));
+    if (e.residual) t.residual = half_bits_to_float(__ldcg(e.residual + m * N + n));
+    return t;
+}
+__device__ __forceinline__ float epilogue_value(float v, const Epilogue &e, const EpilogueTerms &t) {
+    if (e.bias) v += t.bias;
     v = activate(v, e.act);
-    if (e.residual) v += half_bits_to_float(__ldcg(e.residual + m * N + n));
-    return v;
+    return e.residual ? v + t.residual : v;  // (a -0 stays one without a residual)
 }
 
 }  // namespace bonsai

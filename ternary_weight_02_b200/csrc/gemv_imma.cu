@@ -467,6 +467,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_imma_kernel(
         const int tile_first = rt * KC, tile_end = tile_first + KC;
 #pragma unroll
         for (int m = 0; m < kM; m++) {
+            EpilogueTerms terms;
+            if (kEpi && a == tile_first && rt * kItemRows + lane < N)  // (on their way during the sums and the waits)
+                terms = epilogue_terms(epi, m, rt * kItemRows + lane, N);
             float sum = 0.f;
             for (int i = a; i < b; i++) sum += slots[((i - c0) * kM + m) * kItemRows + lane];
             if (a > tile_first) {
@@ -490,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_imma_kernel(
             }
             const int row = rt * kItemRows + lane;
             if (row < N) {
-                if (kEpi) sum = epilogue_value(sum, epi, m, row, N);
+                if (kEpi) sum = epilogue_value(sum, epi, terms);
                 y[(int64_t)m * N + row] = float_to_half_bits(sum);
             }
         }

@@ -408,7 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_split_kernel(
         const int row = lane & 15;
         if (lane < 16 && n0 + row < N) {
             if (S == 1)
-                y[n0 + row] = float_to_half_bits(kEpi ? epilogue_value(total, epi, 0, n0 + row, N) : total);
+                y[n0 + row] = float_to_half_bits(
+                    kEpi ? epilogue_value(total, epi, epilogue_terms(epi, 0, n0 + row, N)) : total);
             else
                 partials[(int64_t)slice * N + n0 + row] = total;
         }
@@ -440,6 +441,8 @@ __global__ void __launch_bounds__(256) gemv_reduce_kernel(const float *__restric
     pdl_launch_dependents();
     pdl_wait();
     for (int64_t n = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; n < N; n += (int64_t)gridDim.x * blockDim.x) {
+        EpilogueTerms terms;
+        if (kEpi) terms = epilogue_terms(epi, 0, n, N);
         float acc = 0.f;
         int s = 0;
         for (; s + 8 <= S; s += 8) {
@@ -450,7 +453,7 @@ __global__ void __launch_bounds__(256) gemv_reduce_kernel(const float *__restric
             for (int u = 0; u < 8; u++) acc += t[u];
         }
         for (; s < S; s++) acc += __ldcg(partials + (int64_t)s * N + n);
-        if (kEpi) acc = epilogue_value(acc, epi, 0, n, N);
+        if (kEpi) acc = epilogue_value(acc, epi, terms);
         y[n] = float_to_half_bits(acc);
     }
 }
@@ -528,7 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_rows_kernel(
         const int64_t n0 = rb * kRows;
         const int row = lane & 15;
         if (active && lane < 16 && n0 + row < N)
-            y[n0 + row] = float_to_half_bits(kEpi ? epilogue_value(total, epi, 0, n0 + row, N) : total);
+            y[n0 + row] = float_to_half_bits(
+                    kEpi ? epilogue_value(total, epi, epilogue_terms(epi, 0, n0 + row, N)) : total);
     }
 }
 

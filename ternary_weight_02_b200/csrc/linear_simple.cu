@@ -69,7 +69,8 @@ __global__ void __launch_bounds__(256) linear_simple_kernel(
         for (int i = 0; i < kTokensPerWarp; i++) {
             const float total = warp_sum(acc[i]);
             if (lane == 0 && m0 + i < M)
-                y[(m0 + i) * N + n] = float_to_half_bits(epilogue_value(total, epi, m0 + i, n, N));
+                y[(m0 + i) * N + n] =
+                    float_to_half_bits(epilogue_value(total, epi, epilogue_terms(epi, m0 + i, n, N)));
         }
     }
 }

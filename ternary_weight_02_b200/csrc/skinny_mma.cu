@@ -584,6 +584,17 @@ __global__ void __launch_bounds__(kThreads) skinny_kernel(
     // ---- output (warps wholly past N do nothing; every CTA of the row block agrees)
     if (n0 >= N) return;
     if (S == 1) {
+        EpilogueTerms terms[NT][4];
+        if constexpr (kEpi) {
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int m = nt * 8 + 2 * tq + (e & 1);
+                    const int64_t r = e < 2 ? r0 : r1;
+                    if (m < M && r < N) terms[nt][e] = epilogue_terms(epi, m, r, N);
+                }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; nt++)
 #pragma unroll
@@ -591,7 +602,7 @@ __global__ void __launch_bounds__(kThreads) skinny_kernel(
                 const int m = nt * 8 + 2 * tq + (e & 1);
                 const int64_t r = e < 2 ? r0 : r1;
                 if (m < M && r < N) {
-                    const float v = kEpi ? epilogue_value(acc[nt][e], epi, m, r, N) : acc[nt][e];
+                    const float v = kEpi ? epilogue_value(acc[nt][e], epi, terms[nt][e]) : acc[nt][e];
                     y[(int64_t)m * N + r] = float_to_half_bits(v);
                 }
             }
@@ -614,14 +625,32 @@ __global__ void __launch_bounds__(kThreads) skinny_kernel(
     if (arrived != (unsigned int)(S - 1)) return;
     __threadfence();
     // last chunk of this row block: sum the partials in chunk order
-    for (int idx = lane; idx < 16 * M; idx += 32) {
-        const int m = idx / 16;
-        const int64_t r = n0 + (idx & 15);
-        if (r >= N) continue;
-        float a = 0.f;
-        for (int c = 0; c < S; c++) a += __ldcg(partials + ((int64_t)c * M + m) * N + r);
-        if (kEpi) a = epilogue_value(a, epi, m, r, N);
-        y[(int64_t)m * N + r] = float_to_half_bits(a);
+    if constexpr (!kEpi) {
+        for (int idx = lane; idx < 16 * M; idx += 32) {
+            const int m = idx / 16;
+            const int64_t r = n0 + (idx & 15);
+            if (r >= N) continue;
+            float a = 0.f;
+            for (int c = 0; c < S; c++) a += __ldcg(partials + ((int64_t)c * M + m) * N + r);
+            y[(int64_t)m * N + r] = float_to_half_bits(a);
+        }
+    } else {
+        EpilogueTerms terms[MT / 2];  // of this lane's outputs idx = lane + 32 i
+#pragma unroll
+        for (int i = 0; i < MT / 2; i++) {
+            const int idx = lane + 32 * i;
+            if (idx < 16 * M && n0 + (idx & 15) < N) terms[i] = epilogue_terms(epi, idx / 16, n0 + (idx & 15), N);
+        }
+#pragma unroll
+        for (int i = 0; i < MT / 2; i++) {
+            const int idx = lane + 32 * i;
+            const int m = idx / 16;
+            const int64_t r = n0 + (idx & 15);
+            if (idx >= 16 * M || r >= N) continue;
+            float a = 0.f;
+            for (int c = 0; c < S; c++) a += __ldcg(partials + ((int64_t)c * M + m) * N + r);
+            y[(int64_t)m * N + r] = float_to_half_bits(epilogue_value(a, epi, terms[i]));
+        }
     }
     if (lane == 0) counters[rb] = 0u;
 }
