@@ -19,7 +19,8 @@
 //   CTAs of two 32 KB stages per SM beat two of three (64 ragged sequences 82 against 86 us):
 //   the consumers' latency, not the bytes in flight, is what more of them hides.
 // * kWarps consumer warps take 16 keys of each tile (two blocks of 16 where a row has 128 bytes
-//   or fewer: E4M3 ragged 96 against 103 us): S^T = K Q^T as m16n8k16 MMAs with the keys as
+//   or fewer: E4M3 ragged 96 against 103 us; one again where 16 query heads of 128 fill the
+//   registers, so that two CTAs fit: 16 heads per key head, E4M3, 68 against 74 us): S^T = K Q^T as m16n8k16 MMAs with the keys as
 //   rows, so that 8 query heads fill the columns and no row is wasted on padding; the
 //   probabilities are rounded to FP16 (2^-11 of each at most, the size of the output's own
 //   rounding), transposed by movmatrix into the B operand of O^T += V^T P^T.  Each warp keeps
@@ -46,12 +47,14 @@ constexpr int kThreads = 32 * (kWarps + 1);
 // parts: 87.9 us in groups, 92.8 us at once; 1024 keys, 16 parts: 10.4 against 9.0 us.)
 constexpr int kFlatParts = 20;
 
-template <int D, int kType>
+template <int D, int kType, int NT>
 struct Cfg {
     static constexpr int kRowBytes = kType == 0 ? 2 * D : D;
     static constexpr int kInner = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a box row
-    static constexpr int kBlk = kRowBytes <= 128 ? 2 : 1;             // 16-key blocks of a warp in a tile
+    static constexpr int kBlk = kRowBytes <= 128 && NT * D <= 128 ? 2 : 1;  // 16-key blocks of a warp in a tile
     static constexpr int kTile = 16 * kWarps * kBlk;                  // keys of a tile
+    // CTAs per SM that the registers leave room for (the ring takes the rest of the shared memory)
+    static constexpr int kCtas = D == 256 ? (NT == 2 || kType == 0 ? 1 : 2) : NT == 2 && D == 128 ? 2 : NT == 1 && D == 64 ? 4 : 3;
     static constexpr int kPoolBytes = kTile * kRowBytes;              // one pool's part of a stage
     static constexpr int kStageBytes = 2 * kPoolBytes;
     static constexpr int kStages = kStageBytes > 32768 ? 3 : kStageBytes > 16384 ? 2 : 4;
@@ -62,7 +65,7 @@ struct Layout {
 };
 template <int D, int kType, int NT>
 constexpr Layout layout() {
-    using C = Cfg<D, kType>;
+    using C = Cfg<D, kType, NT>;
     Layout l{};
     l.join = C::kStages * C::kStageBytes;            // 2 x [NT][D / 16][32] float4
     l.ml = l.join + 2 * 8 * NT * D * 4;              // m and l: [2][kWarps][8 NT]
@@ -201,9 +204,9 @@ struct Walk {
 };
 
 template <int D, int kType, int NT>
-__global__ void __launch_bounds__(kThreads) attention_kernel(const __grid_constant__ CUtensorMap k_map,
+__global__ void __launch_bounds__(kThreads, Cfg<D, kType, NT>::kCtas) attention_kernel(const __grid_constant__ CUtensorMap k_map,
                                                              const __grid_constant__ CUtensorMap v_map, Params p) {
-    using C = Cfg<D, kType>;
+    using C = Cfg<D, kType, NT>;
     constexpr Layout L = layout<D, kType, NT>();
     constexpr int kTile = C::kTile, kBlk = C::kBlk;
     constexpr int kQ = 8 * NT;                 // query heads of an item
@@ -800,7 +803,7 @@ cudaError_t encode_pool(CUtensorMap *map, const void *pool, const KvCache &c, in
 
 template <int D, int kType, int NT>
 cudaError_t launch(Params &p, const KvCache &c, cudaStream_t s, const DeviceInfo &dev) {
-    using C = Cfg<D, kType>;
+    using C = Cfg<D, kType, NT>;
     CUtensorMap k_map, v_map;
     cudaError_t e = encode_pool(&k_map, c.k, c, C::kRowBytes, C::kInner, C::kTile);
     if (e == cudaSuccess) e = encode_pool(&v_map, c.v, c, C::kRowBytes, C::kInner, C::kTile);
