@@ -261,23 +261,25 @@ def bonsai_ternary_linear_swiglu(x, packed, scales, h, M: int, F: int, K: int, f
                                              _stream(stream)), "bonsai_ternary_linear_swiglu")
 
 
-_ANY = None  # no dtype or size to check
+# bytes of a packed 128-weight group, and its scales
+_GROUP_BYTES = {BONSAI_FMT_PTQ1_0: (26, 1), BONSAI_FMT_PQ2_0: (32, 1), BONSAI_FMT_Q1_0: (16, 1),
+                BONSAI_FMT_PQ2_0_G64: (32, 2)}
 
 
-def _dev(t, dtype, numel: int, dev: int, contiguous: bool = True):
-    """Device pointer of a tensor on device `dev`, with the type and at least the size the call
-    reads or writes.  None and plain device pointers pass as they are."""
+def _dev(t, dtype, numel: int, dev: int):
+    """Device pointer of a contiguous tensor on device `dev`, with the type and at least the size
+    the call reads or writes.  None and plain device pointers pass as they are."""
     if t is None or type(t) is int:
         return t
+    if t.get_device() == dev and t.dtype is dtype and t.is_contiguous() and t.numel() >= numel:
+        return t.data_ptr()
     if t.get_device() != dev:
         raise ValueError("tensor arguments must be CUDA tensors on the current device")
-    if t.dtype is not dtype and dtype is not _ANY:
+    if t.dtype is not dtype:
         raise ValueError(f"a tensor argument is {t.dtype} where {dtype} is expected")
-    if contiguous and not t.is_contiguous():
+    if not t.is_contiguous():
         raise ValueError("tensor arguments must be contiguous")
-    if t.numel() < numel:
-        raise ValueError(f"a tensor argument has {t.numel()} elements where the call takes {numel}")
-    return t.data_ptr()
+    raise ValueError(f"a tensor argument has {t.numel()} elements where the call takes {numel}")
 
 
 def _rows(t, rows: int, width: int, ld, dev: int):
@@ -286,23 +288,19 @@ def _rows(t, rows: int, width: int, ld, dev: int):
     if t is None or type(t) is int:
         return t, width if ld is None else ld
     import torch
-    if t.get_device() != dev:
-        raise ValueError("tensor arguments must be CUDA tensors on the current device")
-    if t.dtype is not torch.float16:
-        raise ValueError(f"a tensor argument is {t.dtype} where torch.float16 is expected")
     n = t.numel()
     if t.is_contiguous():
         if ld is None:
             ld = width if n == rows * width or rows == 0 else n // rows
-        if n < (rows - 1) * ld + width:
-            raise ValueError("a tensor of heads is smaller than the call takes")
-    elif t.dim() != 2 or t.stride(1) != 1:
+        return _dev(t, torch.float16, (rows - 1) * ld + width if rows > 0 else 0, dev), ld
+    if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError("a strided tensor of heads is a matrix with contiguous rows")
-    else:
-        if ld is None:
-            ld = t.stride(0)
-        if t.shape[0] < rows or t.shape[1] < width or t.stride(0) != ld:
-            raise ValueError("a strided tensor of heads is smaller than the call takes")
+    if ld is None:
+        ld = t.stride(0)
+    if t.shape[0] < rows or t.shape[1] < width or t.stride(0) != ld:
+        raise ValueError("a strided tensor of heads is smaller than the call takes")
+    if t.get_device() != dev or t.dtype is not torch.float16:
+        raise ValueError("tensor arguments must be float16 CUDA tensors on the current device")
     return t.data_ptr(), ld
 
 
@@ -312,8 +310,10 @@ def bonsai_ternary_linear_epilogue(x, packed, scales, bias, residual, y, M: int,
     """y = act(x' . Wdeq^T + bias) + residual; bias and residual may be None, residual may be y."""
     import torch
     dev, f16 = torch.cuda.current_device(), torch.float16
+    plane, groups = _GROUP_BYTES.get(fmt, (0, 0))
     _check(_call.bonsai_ternary_linear_epilogue(
-        _dev(x, f16, M * K, dev), _dev(packed, torch.uint8, 0, dev), _dev(scales, f16, 0, dev), _dev(bias, f16, N, dev),
+        _dev(x, f16, M * K, dev), _dev(packed, torch.uint8, N * (K // 128) * plane, dev),
+        _dev(scales, f16, N * (K // 128) * groups, dev), _dev(bias, f16, N, dev),
         _dev(residual, f16, M * N, dev), _dev(y, f16, M * N, dev), M, N, K, fmt, act, algo, split_k, _stream_on(stream, dev)),
         "bonsai_ternary_linear_epilogue")
 

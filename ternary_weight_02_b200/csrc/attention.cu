@@ -19,7 +19,7 @@
 //   CTAs of two 32 KB stages per SM beat two of three (64 ragged sequences 82 against 86 us):
 //   the consumers' latency, not the bytes in flight, is what more of them hides.
 // * kWarps consumer warps take 16 keys of each tile (two blocks of 16 where a row has 128 bytes
-//   or fewer: E4M3 ragged 96 against 103 us; one again where 16 query heads of 128 fill the
+//   or fewer: E4M3 ragged 96 against 103 us; four of 64 bytes; one again where 16 query heads of 128 fill the
 //   registers, so that two CTAs fit: 16 heads per key head, E4M3, 68 against 74 us): S^T = K Q^T as m16n8k16 MMAs with the keys as
 //   rows, so that 8 query heads fill the columns and no row is wasted on padding; the
 //   probabilities are rounded to FP16 (2^-11 of each at most, the size of the output's own
@@ -51,10 +51,12 @@ template <int D, int kType, int NT>
 struct Cfg {
     static constexpr int kRowBytes = kType == 0 ? 2 * D : D;
     static constexpr int kInner = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a box row
-    static constexpr int kBlk = kRowBytes <= 128 && NT * D <= 128 ? 2 : 1;  // 16-key blocks of a warp in a tile
+    // 16-key blocks of a warp in a tile: more for short rows, whose keys cost more than their bytes
+    static constexpr int kBlk = kRowBytes == 64 && NT == 1 ? 4 : kRowBytes <= 128 && NT * D <= 128 ? 2 : 1;
     static constexpr int kTile = 16 * kWarps * kBlk;                  // keys of a tile
     // CTAs per SM that the registers leave room for (the ring takes the rest of the shared memory)
-    static constexpr int kCtas = D == 256 ? (NT == 2 || kType == 0 ? 1 : 2) : NT == 2 && D == 128 ? 2 : NT == 1 && D == 64 ? 4 : 3;
+    static constexpr int kCtas = D == 256 ? (NT == 2 || kType == 0 ? 1 : 2)
+                                 : NT == 2 && D == 128 ? 2 : NT == 1 && D == 64 && kType == 0 ? 4 : 3;
     static constexpr int kPoolBytes = kTile * kRowBytes;              // one pool's part of a stage
     static constexpr int kStageBytes = 2 * kPoolBytes;
     static constexpr int kStages = kStageBytes > 32768 ? 3 : kStageBytes > 16384 ? 2 : 4;
