@@ -1218,15 +1218,28 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int tile_hint, int sm_count)
     return p;
 }
 
-// Calls with an epilogue split a tile's K stages over fewer CTAs when there are few tiles: a
-// stage costs about 0.55 us per accumulator, a further piece about 2 us (its 128 KB of sums go
-// through the L2 to the tile's owner), so p pieces of nk stages take 0.55 nk / p + 2 p, least at
-// p = sqrt(0.275 nk).
-int64_t epilogue_ctas(const GemmPlan &p) {
-    int64_t pieces = (int64_t)(std::sqrt(0.275 * (double)p.nk) + 0.5);
-    pieces = pieces < 1 ? 1 : pieces;
-    const int64_t c = (int64_t)p.mt * p.nt * pieces;
-    return c < p.ctas ? c : p.ctas;
+// The plan of a call with an epilogue, and an estimate of its time in us.  A stage costs about
+// 0.76 us with one accumulator and 1.2 with two (PTQ1_0 1.17 and 1.57), a further piece of a tile
+// about 2 us per accumulator (its 128 KB of sums go through the L2 to the tile's owner), and a
+// call about 22 beside.  So p pieces of nk stages are worth sqrt(stage nk / 2 per accumulator)
+// CTAs at most, and one accumulator, with its smaller pieces, is right while the CTAs are not full
+// of stages: 1024 x 4096 at M = 512 41 us against 65, 5120 x 5120 at M = 2048 167 against 140.
+GemmPlan gemm_epilogue_plan(int64_t M, int64_t N, int64_t K, int fmt, int tile_hint, int sm_count, double *us) {
+    GemmPlan best = {};
+    *us = 0;
+    for (int acc = 1; acc <= 2; acc++) {
+        if ((tile_hint == 1 || tile_hint == 2) && acc != tile_hint) continue;
+        GemmPlan p = gemm_plan(M, N, K, acc, sm_count);
+        const double stage = acc == 1 ? (fmt == 1 ? 1.17 : 0.76) : (fmt == 1 ? 1.57 : 1.2);
+        const int64_t tiles = (int64_t)p.mt * p.nt;
+        int64_t pieces = (int64_t)(std::sqrt(0.5 * stage * (double)p.nk / acc) + 0.5);
+        pieces = pieces < 1 ? 1 : pieces;
+        if (tiles * pieces < p.ctas) p.ctas = (int)(tiles * pieces);
+        const double split = p.ctas > tiles ? (double)p.ctas / (double)tiles : 1.0;
+        const double t = 22.0 + 2.0 * acc * split + stage * (double)p.units / p.ctas;
+        if (best.ctas == 0 || t < *us) best = p, *us = t;
+    }
+    return best;
 }
 
 constexpr size_t kSlotBytes = (size_t)2 * BM * BN * 4;  // one CTA's FP32 partial tile (two accumulators)
@@ -1235,11 +1248,10 @@ size_t x_rot_bytes(int64_t M, int64_t K) { return (((size_t)M * (size_t)K * 2) +
 
 }  // namespace
 
-double gemm_epilogue_us(int64_t M, int64_t N, int64_t K, const DeviceInfo &dev) {
-    const GemmPlan p = gemm_plan(M, N, K, 0, dev.sm_count);
-    const double ctas = (double)epilogue_ctas(p), tiles = (double)p.mt * p.nt;
-    const double pieces = ctas > tiles ? ctas / tiles : 1.0;
-    return 22.0 + p.acc * (2.0 * pieces + 0.55 * (double)p.units / ctas);
+double gemm_epilogue_us(int64_t M, int64_t N, int64_t K, int fmt, const DeviceInfo &dev) {
+    double us;
+    gemm_epilogue_plan(M, N, K, fmt, 0, dev.sm_count, &us);
+    return us;
 }
 
 bool gemm_supported(int64_t M, int64_t N, int64_t K, int fmt) {
@@ -1266,8 +1278,9 @@ cudaError_t launch_gemm(const uint16_t *x, const uint8_t *packed, const uint16_t
     if (epi && (swiglu || tile_hint == 3)) return cudaErrorInvalidValue;
     const Epilogue ep = epi ? *epi : Epilogue{};
     if (swiglu && N != 2 * swiglu_f) return cudaErrorInvalidValue;
-    GemmPlan plan = gemm_plan(M, N, K, tile_hint, dev.sm_count);
-    if (epi) plan.ctas = (int)epilogue_ctas(plan);
+    double estimate;
+    const GemmPlan plan = epi ? gemm_epilogue_plan(M, N, K, fmt, tile_hint, dev.sm_count, &estimate)
+                              : gemm_plan(M, N, K, tile_hint, dev.sm_count);
     if (ws.data_bytes < gemm_workspace_bytes(M, N, K, fmt, dev) || plan.ctas > kCtlGemmMaxCtas ||
         ws.zeroed_bytes < kCtlRegionBytes)
         return cudaErrorInvalidValue;

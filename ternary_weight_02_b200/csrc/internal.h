@@ -122,7 +122,8 @@ cudaError_t launch_swiglu(const uint16_t *y, uint16_t *h, int64_t M, int64_t F, 
 
 // ---- gemm_tcgen05.cu: prefill
 bool gemm_supported(int64_t M, int64_t N, int64_t K, int fmt);
-double gemm_epilogue_us(int64_t M, int64_t N, int64_t K, const DeviceInfo &dev);  // estimate of a call with an epilogue
+// estimate of a call with an epilogue
+double gemm_epilogue_us(int64_t M, int64_t N, int64_t K, int fmt, const DeviceInfo &dev);
 size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, const DeviceInfo &dev);
 // tile_hint: 0 automatic, 1 one 128-row accumulator per CTA, 2 two (256 rows).  One launch:
 // the rotation of x into the workspace, a grid barrier, the tiles; hand-over flags and the

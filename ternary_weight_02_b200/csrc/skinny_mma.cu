@@ -49,9 +49,9 @@
 //   group (from byte 32tq / 5) come as three aligned 32-bit loads.
 // * Calls with an epilogue (kEpi: bias, activation, residual on the FP32 sums) take larger
 //   batches too, as grid slices of 16 tokens that re-read the weights through the L2: the
-//   batch-independent cost of the GEMM (rotation, grid barrier, hand-over of split tiles: 25
-//   to 80 us) is more than that for small layers.  1001 x 1024, PQ2_0, M = 100: 12 us
-//   against 39; the choice is made by the two kernels' estimated times.
+//   batch-independent cost of the GEMM (rotation, grid barrier, hand-over of split tiles: 20
+//   to 60 us) is more than that for small layers.  1001 x 1024, PQ2_0, M = 128: 11 us
+//   against 46; the choice is made by the two kernels' estimated times.
 #include <cstring>
 
 #include "common.cuh"
