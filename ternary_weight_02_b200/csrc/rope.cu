@@ -10,9 +10,11 @@
 // tokens; each (token, pair) sine and cosine is computed once into shared memory and serves
 // every head, while the first values are already on their way.  A thread's task is 8 pairs of
 // one head, two 16-byte loads and stores half the rotated part apart in both layouts
-// (neighbouring threads then move neighbouring 16 bytes); when 8 pairs do not divide the
-// rotated part (R % 16 != 0) a task is one pair.  8191 tokens of 48 heads of 128: 34.8 us,
-// 5.79 TB/s (89% of the measured copy); with one pair per task 100 us.
+// (neighbouring threads then move neighbouring 16 bytes).  When 8 pairs do not divide the
+// rotated part (R % 16 != 0, !kWhole) the last task has fewer, and in the half layout the
+// partners start inside a 16-byte chunk and move in words or halfwords.  8191 tokens of 48
+// heads of 128: 33.7 us, 5.98 TB/s (91% of the measured copy); with R = 126 interleaved 35.5,
+// half 95 us.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -32,6 +34,7 @@ struct Job {
     int H, D;           // heads rotated: all of x, or (append) query and key heads
     int tokens;         // per CTA
     int per_head, rot;  // tasks of a rotated head; the first `rot` of them rotate
+    int gap, base;      // then `gap` (0 or 1) for elements [R, base), the rest from base on
     int head_shift;     // log2 of per_head, or -1
     int copy_heads, per_copy;  // append: value heads and their tasks
     RopeArgs r;
@@ -68,9 +71,6 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 // value / scale, nearest even, saturated
-__device__ __forceinline__ uint8_t e4m3_of(float v, float scale) {
-    return __nv_cvt_float_to_fp8(v / scale, __NV_SATFINITE, __NV_E4M3);
-}
 __device__ __forceinline__ uint2 e4m3_of8(const float (&v)[8], float scale) {
     uint32_t u[4];
 #pragma unroll
@@ -79,23 +79,73 @@ __device__ __forceinline__ uint2 e4m3_of8(const float (&v)[8], float scale) {
     return make_uint2(u[0] | (u[1] << 16), u[2] | (u[3] << 16));
 }
 
+// Up to 8 elements from element `at` of a row (16-byte aligned): whole chunks in one access.
+template <bool kWhole>
+__device__ __forceinline__ uint4 load8(const uint16_t *row, int at, int n) {
+    const uint16_t *p = row + at;
+    if (kWhole || (n == 8 && (at & 7) == 0)) return *reinterpret_cast<const uint4 *>(p);
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (n == 8 && (at & 1) == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (i < n) w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <bool kWhole>
+__device__ __forceinline__ void store8(uint16_t *row, int at, int n, const float (&v)[8]) {
+    uint16_t *p = row + at;
+    const uint4 u = pack8(v);
+    if (kWhole || (n == 8 && (at & 7) == 0)) {
+        *reinterpret_cast<uint4 *>(p) = u;
+        return;
+    }
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if (n == 8 && (at & 1) == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) reinterpret_cast<uint32_t *>(p)[i] = w[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (i < n) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    }
+}
+template <bool kWhole>
+__device__ __forceinline__ void store8_e4m3(uint8_t *row, int at, int n, const float (&v)[8], float scale) {
+    uint8_t *p = row + at;
+    const uint2 u = e4m3_of8(v, scale);
+    if (kWhole || (n == 8 && (at & 7) == 0)) {
+        *reinterpret_cast<uint2 *>(p) = u;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        if (i < n) p[i] = (uint8_t)((i < 4 ? u.x : u.y) >> (8 * (i & 3)));
+}
+
 // kMode: 0 rotation alone, 1 append to an FP16 cache, 2 to an E4M3 cache.
-// kVec: elements of a task's chunk, 8 or 1.
-template <int kMode, int kLayout, int kVec>
+// kWhole: R % 16 == 0.
+template <int kMode, int kLayout, bool kWhole>
 __global__ void __launch_bounds__(kMaxThreads) rope_kernel(Job job) {
-    // cosines and sines: [token of the CTA][R / 2], the eight pairs of rotating task k as four
+    // cosines and sines: [token of the CTA][8 rot], the eight pairs of rotating task k as four
     // float4s at k, rot + k, 2 rot + k, 3 rot + k (neighbouring threads read neighbouring words)
     extern __shared__ __align__(16) float2 turn[];
     pdl_launch_dependents();
     pdl_wait();  // everything read or written here may belong to the previous kernel
-    const int half = job.r.R / 2;
+    const int half = job.r.R / 2, turn_stride = 8 * job.rot;
+    const int chunks = (half + 3) >> 2;  // interleaved: 16-byte chunks with pairs
     const int64_t t0 = (int64_t)blockIdx.x * job.tokens;
     const int nt = (int)(job.T - t0 < job.tokens ? job.T - t0 : job.tokens);
     const int rot_tasks = job.H * job.per_head, per_token = rot_tasks + job.copy_heads * job.per_copy;
     const int total = nt * per_token;
 
     struct Task {
-        int token, head, at0, at1, pair;  // elements of the two chunks in the head (at1 < 0: one), first pair (-1: copy)
+        int token, head;
+        int at0, n0, at1, n1;  // first elements of the two chunks in the head, and their elements (0: none)
+        int task;              // which of the head's rotating tasks, or -1: a copy
     };
     auto task_of = [&](int u) {
         Task k;
@@ -105,25 +155,32 @@ __global__ void __launch_bounds__(kMaxThreads) rope_kernel(Job job) {
             u -= k.token * per_token;
         }
         int i;
+        bool value = false;
         if (kMode == 0 || u < rot_tasks) {
             k.head = job.head_shift >= 0 ? u >> job.head_shift : u / job.per_head;
             i = u - k.head * job.per_head;
         } else {
             u -= rot_tasks;
             k.head = u / job.per_copy;
-            i = u - k.head * job.per_copy + job.rot;
+            i = u - k.head * job.per_copy;
             k.head += job.H;
+            value = true;
         }
-        const bool value = kMode != 0 && k.head >= job.H;
+        k.task = -1;
+        k.n0 = k.n1 = 8;
         if (!value && i < job.rot) {
-            k.pair = i * kVec;
+            k.task = i;
             // half: elements 8i .. and their partners; interleaved: 16-byte chunks i and rot + i
-            k.at0 = kLayout == 0 || kVec == 8 ? k.pair : 2 * k.pair;
-            k.at1 = kLayout == 0 || kVec == 8 ? k.pair + half : 2 * k.pair + 1;
+            k.at0 = 8 * i;
+            k.at1 = kLayout == 0 ? 8 * i + half : 8 * (job.rot + i);
+            if (!kWhole && kLayout == 0) k.n0 = k.n1 = half - 8 * i < 8 ? half - 8 * i : 8;
+            if (!kWhole && kLayout == 1 && job.rot + i >= chunks) k.n1 = 0;
+        } else if (!kWhole && !value && i < job.rot + job.gap) {
+            k.at0 = k.at1 = job.r.R, k.n0 = job.base - job.r.R, k.n1 = 0;
         } else {
-            k.pair = -1;
-            k.at0 = (value ? 0 : job.r.R) + (i - job.rot) * 2 * kVec;
-            k.at1 = k.at0 + kVec < job.D ? k.at0 + kVec : -1;
+            k.at0 = value ? 16 * i : job.base + 16 * (i - job.rot - job.gap);
+            k.at1 = k.at0 + 8;
+            if (k.at1 >= job.D) k.n1 = 0;
         }
         return k;
     };
@@ -141,13 +198,8 @@ __global__ void __launch_bounds__(kMaxThreads) rope_kernel(Job job) {
             if (u >= total) continue;
             const Task k = task_of(u);
             const uint16_t *row = row_of(k);
-            if constexpr (kVec == 8) {
-                w0[j] = *reinterpret_cast<const uint4 *>(row + k.at0);
-                if (k.at1 >= 0) w1[j] = *reinterpret_cast<const uint4 *>(row + k.at1);
-            } else {
-                w0[j].x = row[k.at0];
-                if (k.at1 >= 0) w1[j].x = row[k.at1];
-            }
+            w0[j] = load8<kWhole>(row, k.at0, k.n0);
+            if (k.n1 > 0) w1[j] = load8<kWhole>(row, k.at1, k.n1);
             sc[j] = 1.f;
             if (kMode == 2 && k.head >= job.Hq)
                 sc[j] = __ldcg((k.head < job.H ? job.c.k_scale : job.c.v_scale) + kv_head(k));
@@ -157,18 +209,14 @@ __global__ void __launch_bounds__(kMaxThreads) rope_kernel(Job job) {
     for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
         const int token = i / half;
         const int pair = i - token * half;
-        int at = pair;
-        if constexpr (kVec == 8) {
-            int task, quarter;  // of the pair's float4
-            if (kLayout == 0) {
-                task = pair >> 3, quarter = (pair & 7) >> 1;
-            } else {
-                const int chunk = pair >> 2, second = chunk >= job.rot;
-                task = second ? chunk - job.rot : chunk, quarter = 2 * second + ((pair & 3) >> 1);
-            }
-            at = (quarter * job.rot + task) * 2 + (pair & 1);
+        int task, quarter;  // of the pair's float4
+        if (kLayout == 0) {
+            task = pair >> 3, quarter = (pair & 7) >> 1;
+        } else {
+            const int chunk = pair >> 2, second = chunk >= job.rot;
+            task = second ? chunk - job.rot : chunk, quarter = 2 * second + ((pair & 3) >> 1);
         }
-        turn[token * half + at] =
+        turn[token * turn_stride + (quarter * job.rot + task) * 2 + (pair & 1)] =
             sincos_at(__ldcg(job.r.positions + t0 + token), __ldcg(job.r.freqs + pair), job.r.magnitude);
     }
     // row of the tokens' entries in the pools' first head (or -1), in rows of D elements
@@ -181,55 +229,41 @@ __global__ void __launch_bounds__(kMaxThreads) rope_kernel(Job job) {
     }
     __syncthreads();
     auto finish = [&](const Task &k, const uint4 &c0, const uint4 &c1, float scale) {
-        constexpr int n = kVec;
         float a[8], b[8];
-        if constexpr (n == 8) {
-            unpack8(c0, a);
-            unpack8(c1, b);
-        } else {
-            a[0] = half_bits_to_float((uint16_t)c0.x), b[0] = half_bits_to_float((uint16_t)c1.x);
-        }
-        if (k.pair >= 0) {
-            const float2 *cs = turn + k.token * half;
-            if constexpr (n == 1) {
-                const float2 f = cs[k.pair];
-                const float p = a[0], q = b[0];
-                a[0] = p * f.x - q * f.y;
-                b[0] = q * f.x + p * f.y;
-            } else {
-                float2 f[8];
+        unpack8(c0, a);
+        unpack8(c1, b);
+        if (k.task >= 0) {
+            const float4 *cs = reinterpret_cast<const float4 *>(turn + k.token * turn_stride) + k.task;
+            float2 f[8];
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const float4 v = reinterpret_cast<const float4 *>(cs)[i * job.rot + k.pair / 8];
-                    f[2 * i] = make_float2(v.x, v.y), f[2 * i + 1] = make_float2(v.z, v.w);
+            for (int i = 0; i < 4; i++) {
+                const float4 v = cs[i * job.rot];
+                f[2 * i] = make_float2(v.x, v.y), f[2 * i + 1] = make_float2(v.z, v.w);
+            }
+            if constexpr (kLayout == 0) {
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const float p = a[i], q = b[i];
+                    a[i] = p * f[i].x - q * f[i].y;
+                    b[i] = q * f[i].x + p * f[i].y;
                 }
-                if constexpr (kLayout == 0) {
-#pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        const float p = a[i], q = b[i];
-                        a[i] = p * f[i].x - q * f[i].y;
-                        b[i] = q * f[i].x + p * f[i].y;
-                    }
-                } else {
+            } else {
+                auto rotate = [&](float (&v)[8], const float2 *g, int first) {  // pairs first .. of a chunk
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
-                        const float p = a[2 * i], q = a[2 * i + 1], r = b[2 * i], t = b[2 * i + 1];
-                        a[2 * i] = p * f[i].x - q * f[i].y;
-                        a[2 * i + 1] = q * f[i].x + p * f[i].y;
-                        b[2 * i] = r * f[i + 4].x - t * f[i + 4].y;
-                        b[2 * i + 1] = t * f[i + 4].x + r * f[i + 4].y;
+                        if (!kWhole && first + i >= half) continue;  // (elements that are not rotated)
+                        const float p = v[2 * i], q = v[2 * i + 1];
+                        v[2 * i] = p * g[i].x - q * g[i].y;
+                        v[2 * i + 1] = q * g[i].x + p * g[i].y;
                     }
-                }
+                };
+                rotate(a, f, 4 * k.task);
+                rotate(b, f + 4, 4 * (job.rot + k.task));
             }
         }
         auto put16 = [&](uint16_t *row) {
-            if constexpr (n == 8) {
-                *reinterpret_cast<uint4 *>(row + k.at0) = pack8(a);
-                if (k.at1 >= 0) *reinterpret_cast<uint4 *>(row + k.at1) = pack8(b);
-            } else {
-                row[k.at0] = float_to_half_bits(a[0]);
-                if (k.at1 >= 0) row[k.at1] = float_to_half_bits(b[0]);
-            }
+            store8<kWhole>(row, k.at0, k.n0, a);
+            if (k.n1 > 0) store8<kWhole>(row, k.at1, k.n1, b);
         };
         if (kMode == 0 || k.head < job.Hq) {
             put16(job.out + (t0 + k.token) * job.ld_out + (int64_t)k.head * job.D);
@@ -241,13 +275,8 @@ __global__ void __launch_bounds__(kMaxThreads) rope_kernel(Job job) {
                     put16(static_cast<uint16_t *>(pool) + at);
                 } else {
                     uint8_t *row = static_cast<uint8_t *>(pool) + at;
-                    if constexpr (n == 8) {
-                        *reinterpret_cast<uint2 *>(row + k.at0) = e4m3_of8(a, scale);
-                        if (k.at1 >= 0) *reinterpret_cast<uint2 *>(row + k.at1) = e4m3_of8(b, scale);
-                    } else {
-                        row[k.at0] = e4m3_of(a[0], scale);
-                        if (k.at1 >= 0) row[k.at1] = e4m3_of(b[0], scale);
-                    }
+                    store8_e4m3<kWhole>(row, k.at0, k.n0, a, scale);
+                    if (k.n1 > 0) store8_e4m3<kWhole>(row, k.at1, k.n1, b, scale);
                 }
             }
         }
@@ -266,13 +295,16 @@ __global__ void __launch_bounds__(kMaxThreads) rope_kernel(Job job) {
 template <int kMode>
 cudaError_t launch(Job &job, cudaStream_t s, const DeviceInfo &dev) {
     const int R = job.r.R, D = job.D;
-    const bool vec = R % 16 == 0;
-    const int v = vec ? 8 : 1;
-    job.rot = R / 2 / v;
+    const bool whole = R % 16 == 0, halves = job.r.layout == 0;
+    const int chunks = (R / 2 + 3) / 4;
+    job.rot = halves ? (R / 2 + 7) / 8 : (chunks + 1) / 2;
+    job.base = halves ? (R + 7) / 8 * 8 : 8 * chunks;
+    job.gap = halves && R % 8 != 0;
     // in place, what is not rotated already is where it belongs
     const bool in_place = kMode == 0 && job.x == job.out;
-    job.per_head = job.rot + (in_place ? 0 : (D - R + 2 * v - 1) / (2 * v));
-    job.per_copy = (D + 2 * v - 1) / (2 * v);
+    job.per_head = job.rot + (in_place ? 0 : job.gap + (D - job.base + 15) / 16);
+    if (in_place) job.gap = 0;
+    job.per_copy = (D + 15) / 16;
     const int64_t per_token = (int64_t)job.H * job.per_head + (int64_t)job.copy_heads * job.per_copy;
     if (per_token == 0) return cudaSuccess;
     // several small tokens per CTA, as long as every SM still gets four CTAs
@@ -292,16 +324,16 @@ cudaError_t launch(Job &job, cudaStream_t s, const DeviceInfo &dev) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((job.T + tokens - 1) / tokens));
     cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = (size_t)tokens * (size_t)(R / 2) * sizeof(float2);
+    cfg.dynamicSmemBytes = (size_t)tokens * (size_t)(8 * job.rot) * sizeof(float2);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (vec)
-        return cudaLaunchKernelEx(&cfg, job.r.layout == 0 ? rope_kernel<kMode, 0, 8> : rope_kernel<kMode, 1, 8>, job);
-    return cudaLaunchKernelEx(&cfg, job.r.layout == 0 ? rope_kernel<kMode, 0, 1> : rope_kernel<kMode, 1, 1>, job);
+    if (whole)
+        return cudaLaunchKernelEx(&cfg, halves ? rope_kernel<kMode, 0, true> : rope_kernel<kMode, 1, true>, job);
+    return cudaLaunchKernelEx(&cfg, halves ? rope_kernel<kMode, 0, false> : rope_kernel<kMode, 1, false>, job);
 }
 
 }  // namespace
