@@ -213,6 +213,42 @@ __global__ void __launch_bounds__(256) skinny_prep_kernel(const uint16_t *__rest
 }
 
 
+// Calls with an epilogue, split-K: one warp sums the chunks' partials of a 16-row block in chunk
+// order.  This lane's outputs are tokens lane / 16 + 2 i of row n0 + lane % 16; their bias and
+// residual and all partials are read before the first store.  With 16 tokens it is not inlined:
+// its registers would be those that the kernel's main loop is scheduled with (16 tokens of 1024 x
+// 4096: 18.5 us inlined, 12.8 not; 8 tokens of 5120 x 17408: 18.1 inlined, 18.5 not).
+template <int MT>
+__device__ __forceinline__ void join_chunks_body(const float *partials, uint16_t *y, Epilogue epi, int M, int64_t N, int S,
+                                         int64_t n0, int lane) {
+    const int64_t row = n0 + (lane & 15), r = row < N ? row : N - 1;  // (reads past the outputs go to others)
+    EpilogueTerms terms[MT / 2];
+    float a[MT / 2];
+    const float *src[MT / 2];
+#pragma unroll
+    for (int i = 0; i < MT / 2; i++) {
+        const int m = lane / 16 + 2 * i < M ? lane / 16 + 2 * i : M - 1;
+        a[i] = 0.f;
+        src[i] = partials + (int64_t)m * N + r;
+        terms[i] = epilogue_terms(epi, m, r, N);
+    }
+    const int64_t step = (int64_t)M * N;
+#pragma unroll 4
+    for (int c = 0; c < S; c++)
+#pragma unroll
+        for (int i = 0; i < MT / 2; i++) a[i] += __ldcg(src[i] + c * step);
+#pragma unroll
+    for (int i = 0; i < MT / 2; i++) {
+        const int m = lane / 16 + 2 * i;
+        if (m < M && row < N) y[(int64_t)m * N + row] = float_to_half_bits(epilogue_value(a[i], epi, terms[i]));
+    }
+}
+
+__device__ __noinline__ void join_chunks16(const float *partials, uint16_t *y, Epilogue epi, int M, int64_t N, int S,
+                                           int64_t n0, int lane) {
+    join_chunks_body<16>(partials, y, epi, M, N, S, n0, lane);
+}
+
 // kFmt: 2 PQ2_0, 4 PQ2_0 g64 (64-weight scales), 3 Q1_0, 1 PTQ1_0 (transcoded to PQ2_0 codes)
 //
 // x != nullptr: the rotation is the kernel's first phase.  Every CTA rotates its share of
@@ -228,7 +264,7 @@ __global__ void __launch_bounds__(256) skinny_prep_kernel(const uint16_t *__rest
 // registers or load slots.  wmap and smap are the packed plane's and the scale plane's
 // tensor maps (unused otherwise).  Needs K a multiple of 1024 and chunks of whole stages.
 template <int NT, int kFmt, bool kTma, bool kEpi>  // n8 token tiles: 1 (M <= 8) or 2 (M <= 16)
-__global__ void __launch_bounds__(kThreads) skinny_kernel(
+__global__ void __launch_bounds__(kThreads, (kEpi ? 2 : 0)) skinny_kernel(
     uint16_t *__restrict__ xsg, float *__restrict__ gsg, const uint8_t *__restrict__ packed,
     const uint16_t *__restrict__ scales, uint16_t *__restrict__ y, float *__restrict__ partials,
     unsigned int *__restrict__ counters, int M, int64_t N, int64_t K, int S, int gpc,
@@ -592,7 +628,7 @@ __global__ void __launch_bounds__(kThreads) skinny_kernel(
                 for (int e = 0; e < 4; e++) {
                     const int m = nt * 8 + 2 * tq + (e & 1);
                     const int64_t r = e < 2 ? r0 : r1;
-                    if (m < M && r < N) terms[nt][e] = epilogue_terms(epi, m, r, N);
+                    terms[nt][e] = epilogue_terms(epi, m < M ? m : M - 1, r < N ? r : N - 1, N);
                 }
         }
 #pragma unroll
@@ -635,22 +671,10 @@ __global__ void __launch_bounds__(kThreads) skinny_kernel(
             y[(int64_t)m * N + r] = float_to_half_bits(a);
         }
     } else {
-        EpilogueTerms terms[MT / 2];  // of this lane's outputs idx = lane + 32 i
-#pragma unroll
-        for (int i = 0; i < MT / 2; i++) {
-            const int idx = lane + 32 * i;
-            if (idx < 16 * M && n0 + (idx & 15) < N) terms[i] = epilogue_terms(epi, idx / 16, n0 + (idx & 15), N);
-        }
-#pragma unroll
-        for (int i = 0; i < MT / 2; i++) {
-            const int idx = lane + 32 * i;
-            const int m = idx / 16;
-            const int64_t r = n0 + (idx & 15);
-            if (idx >= 16 * M || r >= N) continue;
-            float a = 0.f;
-            for (int c = 0; c < S; c++) a += __ldcg(partials + ((int64_t)c * M + m) * N + r);
-            y[(int64_t)m * N + r] = float_to_half_bits(epilogue_value(a, epi, terms[i]));
-        }
+        if constexpr (MT == 8)
+            join_chunks_body<8>(partials, y, epi, M, N, S, n0, lane);
+        else
+            join_chunks16(partials, y, epi, M, N, S, n0, lane);
     }
     if (lane == 0) counters[rb] = 0u;
 }
