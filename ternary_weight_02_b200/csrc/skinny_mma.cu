@@ -50,7 +50,7 @@
 // * Calls with an epilogue (kEpi: bias, activation, residual on the FP32 sums) take larger
 //   batches too, as grid slices of 16 tokens that re-read the weights through the L2: the
 //   batch-independent cost of the GEMM (rotation, grid barrier, hand-over of split tiles: 20
-//   to 60 us) is more than that for small layers.  1001 x 1024, PQ2_0, M = 128: 11 us
+//   to 60 us) is more than that for small layers.  1001 x 1024, PQ2_0, M = 128: 8 us
 //   against 46; the choice is made by the two kernels' estimated times.
 #include <cstring>
 
@@ -765,8 +765,8 @@ cudaError_t grid_fits(int64_t M, int64_t N, int64_t K, int fmt, int split_k, con
 }  // namespace
 
 double skinny_groups_us(int64_t M, int64_t N, int64_t K, int fmt) {
-    const double per = fmt == 1 ? 0.34 : fmt == 3 ? 0.15 : fmt == 4 ? 0.22 : 0.20;  // us per 10^6 weights of a group
-    return 14.0 + per * 1e-6 * (double)token_groups(M) * (double)N * (double)K;
+    const double per = fmt == 1 ? 0.42 : fmt == 3 ? 0.165 : fmt == 4 ? 0.23 : 0.19;  // us per 10^6 weights of a group
+    return 8.0 + per * 1e-6 * (double)token_groups(M) * (double)N * (double)K;
 }
 
 bool skinny_groups_supported(int64_t M, int64_t N, int64_t K, int fmt) {
