@@ -330,6 +330,10 @@ __device__ __forceinline__ unsigned int ld_acquire_u32(const unsigned int *p) {
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
+// (kEpi) pieces of a tile whose sums its owner reads at a time: 128 x 5120 x 5120 35.4 us, one
+// at a time 35.9, three 36.0.
+constexpr int kTogether = 2;
+
 // Residual of one warp's 32 rows x 128 columns into its staging rows (16-byte chunks swizzled by
 // the row), two rows of 256 bytes per instruction: a lane later finds its own row's values there,
 // wherever the row starts in memory.  Rows past M and columns past N get zeros.
@@ -892,11 +896,24 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tcgen05_kernel(
             const bool owner = p.kb == 0 && p.ke < nk;        // first piece, others follow
             const int tile_end = (p.tr + 1) * nk;  // in split units
             bool got = true;  // the later pieces all arrived (owner)
-            if (owner)  // (the same rank's CTA of each later unit: its half of the tile)
+            const int w8 = warp - 2;
+            if constexpr (kEpi)  // (before the wait below: 128 x 5120 x 5120 32.9 us, after it 35.4)
+                if (epi.residual && !continues)
+                    stage_residual(sB + w8 * 8192, epi.residual, (int64_t)acc_row0(tm, 0) + 32 * q, M,
+                                   (int64_t)tn * BN + half * 128, N, lane);
+            // kEpi: the tile's later pieces are those of the next `later` CTAs; the warp waits for 32
+            // flags at a time, a lane looking at each (in turn, five flags cost 4 us though all
+            // were up)
+            const int later = kEpi && owner ? (int)(((int64_t)tile_end * nunits - 1) / Ur) - unit : 0;
+            if constexpr (kEpi) {
+                for (int k0 = 0; k0 < later; k0 += 32) {  // (the same trips in every lane: the wait votes)
+                    const int k = k0 + lane < later ? k0 + lane : later - 1;
+                    got = flag_wait(flags + unit + 1 + k, epoch + epoch_skew, wait_limit) && got;
+                }
+            } else if (owner)  // (the same rank's CTA of each later unit: its half of the tile)
                 for (int c2 = unit + 1, s = u_end; s < tile_end; s = range_end(c2), c2++)
                     got = flag_wait(flags + cta_of(c2), epoch + epoch_skew, wait_limit) && got;
             if (!got && r == 0) atomicOr(status, kDevStatusGemmTimeout);
-            const int w8 = warp - 2;
             if constexpr (kSwiglu) {
                 // h columns [64 half, +64) of the tile's 128: gate accumulator columns
                 // 64 half + 32 cc and up columns 128 + 64 half + 32 cc.  Hand-over slots are
@@ -1005,7 +1022,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tcgen05_kernel(
 #pragma unroll 1
             for (int a = 0; a < kAcc; a++) {
                 if constexpr (kEpi) {
-                    if (epi.residual && !continues)
+                    if (a > 0 && epi.residual && !continues)
                         stage_residual(stage_y, epi.residual, (int64_t)acc_row0(tm, a) + 32 * q, M,
                                        (int64_t)tn * BN + half * 128, N, lane);
 #pragma unroll 1
@@ -1029,15 +1046,26 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tcgen05_kernel(
                             continue;
                         }
                         if (owner) {
-                            for (int c2 = unit + 1, s = u_end; s < tile_end; s = range_end(c2), c2++) {
-                                const float4 *src = slot_at(cta_of(c2), a, c);
+                            // kTogether pieces' sums in flight (past the last: the last again,
+                            // not added); added in the order of the pieces
+                            for (int k = 0; k < later; k += kTogether) {
+                                float4 w[kTogether][8];
 #pragma unroll
-                                for (int i = 0; i < 8; i++) {
-                                    const float4 w = __ldcg(src + 32 * i);
-                                    v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + w.x);
-                                    v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + w.y);
-                                    v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + w.z);
-                                    v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + w.w);
+                                for (int u = 0; u < kTogether; u++) {
+                                    const float4 *src = slot_at(unit + 1 + (k + u < later ? k + u : later - 1), a, c);
+#pragma unroll
+                                    for (int i = 0; i < 8; i++) w[u][i] = __ldcg(src + 32 * i);
+                                }
+#pragma unroll
+                                for (int u = 0; u < kTogether; u++) {
+                                    if (k + u >= later) continue;
+#pragma unroll
+                                    for (int i = 0; i < 8; i++) {
+                                        v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + w[u][i].x);
+                                        v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + w[u][i].y);
+                                        v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + w[u][i].z);
+                                        v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + w[u][i].w);
+                                    }
                                 }
                             }
                             if (!got)
