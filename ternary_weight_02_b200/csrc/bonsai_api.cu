@@ -186,8 +186,8 @@ int resolve_algo(int algo, int64_t M, int64_t N, int64_t K, int fmt, const Devic
 // As resolve_algo, for a call with an epilogue: the skinny kernel also takes larger batches there,
 // in groups of 16 tokens that re-read the weights (from the L2, mostly), and the automatic choice
 // compares the two kernels' estimated times.  PQ2_0, us, skinny in groups against GEMM:
-//   1001 x 1024:  M = 32 8.3 / 34, M = 1024 18 / 47;  5120 x 5120: M = 64 30 / 37, M = 128 44 / 38;
-//   5120 x 17408: M = 32 39 / 58, M = 64 88 / 59.
+//   1001 x 1024:  M = 32 8.4 / 27, M = 1024 18 / 38;  5120 x 5120: M = 64 29 / 32, M = 128 45 / 33;
+//   5120 x 17408: M = 32 38 / 49, M = 64 88 / 51.
 int resolve_epilogue_algo(int algo, int64_t M, int64_t N, int64_t K, int fmt, const DeviceInfo *dev = nullptr) {
     if (M > 16 && skinny_groups_supported(M, N, K, fmt)) {
         if (algo == BONSAI_ALGO_SKINNY) return algo;

@@ -1248,10 +1248,13 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int tile_hint, int sm_count)
 
 // The plan of a call with an epilogue, and an estimate of its time in us.  A stage costs about
 // 0.76 us with one accumulator and 1.2 with two (PTQ1_0 1.17 and 1.57), a further piece of a tile
-// about 2 us per accumulator (its 128 KB of sums go through the L2 to the tile's owner), and a
-// call about 22 beside.  So p pieces of nk stages are worth sqrt(stage nk / 2 per accumulator)
-// CTAs at most, and one accumulator, with its smaller pieces, is right while the CTAs are not full
-// of stages: 1024 x 4096 at M = 512 41 us against 65, 5120 x 5120 at M = 2048 167 against 140.
+// about 1.5 us, with two accumulators 4 (its 128 KB of sums per accumulator go through the L2 to
+// the tile's owner), CTAs whose range covers parts of two tiles 4, and a call about 16 beside.  So
+// p pieces of nk stages are worth sqrt(stage nk / 1.5 per accumulator) CTAs at most, the same whole
+// number of them for every tile where that costs few CTAs (128 x 5120 x 17408 52.1 us on 140,
+// 55.3 on 148; PTQ1_0 128 x 5120 x 5120 37.0 and 41.8), and one accumulator, with its smaller
+// pieces, is right while the CTAs are not full of stages: 1024 x 4096 at M = 512 34 us against 65,
+// 5120 x 5120 at M = 2048 167 against 140.
 GemmPlan gemm_epilogue_plan(int64_t M, int64_t N, int64_t K, int fmt, int tile_hint, int sm_count, double *us) {
     GemmPlan best = {};
     *us = 0;
@@ -1259,13 +1262,17 @@ GemmPlan gemm_epilogue_plan(int64_t M, int64_t N, int64_t K, int fmt, int tile_h
         if ((tile_hint == 1 || tile_hint == 2) && acc != tile_hint) continue;
         GemmPlan p = gemm_plan(M, N, K, acc, sm_count);
         const double stage = acc == 1 ? (fmt == 1 ? 1.17 : 0.76) : (fmt == 1 ? 1.57 : 1.2);
-        const int64_t tiles = (int64_t)p.mt * p.nt;
-        int64_t pieces = (int64_t)(std::sqrt(0.5 * stage * (double)p.nk / acc) + 0.5);
+        const int64_t tiles = (int64_t)p.mt * p.nt, all = p.ctas;
+        int64_t pieces = (int64_t)(std::sqrt(0.67 * stage * (double)p.nk / acc) + 0.5);
         pieces = pieces < 1 ? 1 : pieces;
-        if (tiles * pieces < p.ctas) p.ctas = (int)(tiles * pieces);
-        const double split = p.ctas > tiles ? (double)p.ctas / (double)tiles : 1.0;
-        const double t = 22.0 + 2.0 * acc * split + stage * (double)p.units / p.ctas;
-        if (best.ctas == 0 || t < *us) best = p, *us = t;
+        for (int whole = 0; whole <= 1; whole++) {
+            if (whole && all > tiles && pieces > all / tiles) pieces = all / tiles;
+            p.ctas = (int)(tiles * pieces < all ? tiles * pieces : all);
+            const double split = p.ctas > tiles ? (double)p.ctas / (double)tiles : 1.0;
+            const double t = 16.0 + (acc == 1 ? 1.5 : 4.0) * split + stage * (double)p.units / p.ctas +
+                             (p.ctas > tiles && p.ctas % tiles ? 4.0 : 0.0);
+            if (best.ctas == 0 || t < *us) best = p, *us = t;
+        }
     }
     return best;
 }
