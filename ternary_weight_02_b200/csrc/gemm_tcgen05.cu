@@ -1249,7 +1249,8 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int tile_hint, int sm_count)
 // The plan of a call with an epilogue, and an estimate of its time in us.  A stage costs about
 // 0.76 us with one accumulator and 1.2 with two (PTQ1_0 1.17 and 1.57), a further piece of a tile
 // about 1.5 us, with two accumulators 4 (its 128 KB of sums per accumulator go through the L2 to
-// the tile's owner), CTAs whose range covers parts of two tiles 4, and a call about 16 beside.  So
+// the tile's owner), CTAs whose range covers parts of two tiles 4, rows of y and residual that
+// start off 16 bytes 0.1 per row of a tile, and a call about 16 beside.  So
 // p pieces of nk stages are worth sqrt(stage nk / 1.5 per accumulator) CTAs at most, the same whole
 // number of them for every tile where that costs few CTAs (128 x 5120 x 17408 52.1 us on 140,
 // 55.3 on 148; PTQ1_0 128 x 5120 x 5120 37.0 and 41.8), and one accumulator, with its smaller
@@ -1270,7 +1271,8 @@ GemmPlan gemm_epilogue_plan(int64_t M, int64_t N, int64_t K, int fmt, int tile_h
             p.ctas = (int)(tiles * pieces < all ? tiles * pieces : all);
             const double split = p.ctas > tiles ? (double)p.ctas / (double)tiles : 1.0;
             const double t = 16.0 + (acc == 1 ? 1.5 : 4.0) * split + stage * (double)p.units / p.ctas +
-                             (p.ctas > tiles && p.ctas % tiles ? 4.0 : 0.0);
+                             (p.ctas > tiles && p.ctas % tiles ? 4.0 : 0.0) +
+                             (N & 7 ? 0.1 * (double)(M < BM ? M : BM) : 0.0);
             if (best.ctas == 0 || t < *us) best = p, *us = t;
         }
     }
