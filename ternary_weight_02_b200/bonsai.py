@@ -288,10 +288,18 @@ def _rows(t, rows: int, width: int, ld, dev: int):
     if t is None or type(t) is int:
         return t, width if ld is None else ld
     import torch
-    n = t.numel()
     if t.is_contiguous():
-        if ld is None:
-            ld = width if n == rows * width or rows == 0 else n // rows
+        if ld is None:  # a matrix's rows may be wider, or more, than the call takes
+            n = t.numel()
+            if t.dim() == 2 and t.shape[1] >= width:
+                ld = t.shape[1]
+            elif n == rows * width or rows == 0:
+                ld = width
+            elif t.dim() > 1 and t.shape[0] == rows and n > rows * width:
+                ld = n // rows
+            else:
+                raise ValueError("a tensor of heads that is no matrix holds the rows of the call, or the call is given "
+                                 "their stride")
         return _dev(t, torch.float16, (rows - 1) * ld + width if rows > 0 else 0, dev), ld
     if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError("a strided tensor of heads is a matrix with contiguous rows")

@@ -161,3 +161,17 @@ def test_binding_refuses_host_tensors_and_mixed_pools(bz):
                  (pool[0], pool[0])):
         with pytest.raises(ValueError):
             bz.bonsai_paged_attention(q, k, v, None, None, table, n, q, 1, 1)
+
+
+def test_binding_row_strides(bz):
+    """Rows of heads keep their place when the tensor has more or wider rows than the call takes."""
+    import torch
+    def ld(*shape, rows=3, width=64, given=None):
+        return bz._rows(torch.zeros(*shape, dtype=torch.float16), rows, width, given, -1)[1]
+    assert ld(3, 64) == ld(8, 64) == ld(3 * 64) == ld(3, 4, 16) == ld(12, 16) == 64
+    assert ld(3, 96) == ld(8, 96) == ld(3, 6, 16) == 96  # wider rows, more rows
+    assert ld(1, 80, rows=1) == 80 and ld(0, 64, rows=0) == 64
+    assert ld(8 * 64, given=64) == 64 and ld(3 * 128, given=128) == 128
+    for shape, given in (((8, 4, 16), None), ((512,), None), ((2, 64), None), ((100,), None), ((3, 64), 96)):
+        with pytest.raises(ValueError):
+            ld(*shape, given=given)
