@@ -330,10 +330,11 @@ int bonsai_rope_append(const uint16_t *qkv, uint16_t *q_out, void *k_cache, void
  * that is negative or exceeds max_pages * page_size, makes that sequence's outputs NaN and
  * sets BONSAI_DEVICE_CACHE_RANGE; nothing outside the buffers is read.
  *   Statistics, scores and sums are FP32; the probabilities are rounded to FP16 before the
- * product with the values.  Results depend on the lengths and the device's SM count only
+ * product with the values (2^-11 of each; below 2^-28 of a sequence's largest, 2^-39 of that).  Results depend on the lengths and the device's SM count only
  * (bitwise repeatable).  Hq a positive multiple of Hkv; ld_q, ld_out at least Hq * D and
  * multiples of 8; page_table, lengths, lse and the scales aligned to their element; window
- * >= 0.  Uses the workspace: see the conventions above. */
+ * >= 0.  Uses the workspace: see the conventions above (less of it than bonsai_reserve makes
+ * for any shape). */
 int bonsai_paged_attention(const uint16_t *q, const void *k_cache, const void *v_cache, const float *k_scale,
                            const float *v_scale, const int32_t *page_table, const int32_t *lengths,
                            uint16_t *out, float *lse, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,

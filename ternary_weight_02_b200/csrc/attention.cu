@@ -8,7 +8,7 @@
 // it, 4 G flops per FP16 element pair, far below the tensor cores' rate.  So the design serves
 // the copies:
 //
-// * Units of work are tiles of 64 or 128 keys of one (sequence, key/value head, tile of 8 NT query
+// * Units of work are tiles of 64, 128 or 256 keys of one (sequence, key/value head, tile of 8 NT query
 //   heads).  All units of the call lie in one list, sequence by sequence, and each CTA of a
 //   grid that is resident at once takes an equal run of it: a ragged batch loads every SM
 //   alike, one long sequence spreads over all of them, and the host needs no lengths (a
@@ -19,11 +19,11 @@
 //   CTAs of two 32 KB stages per SM beat two of three (64 ragged sequences 82 against 86 us):
 //   the consumers' latency, not the bytes in flight, is what more of them hides.
 // * kWarps consumer warps take 16 keys of each tile (two blocks of 16 where a row has 128 bytes
-//   or fewer: E4M3 ragged 96 against 103 us; four of 64 bytes; one again where 16 query heads of 128 fill the
-//   registers, so that two CTAs fit: 16 heads per key head, E4M3, 68 against 74 us): S^T = K Q^T as m16n8k16 MMAs with the keys as
-//   rows, so that 8 query heads fill the columns and no row is wasted on padding; the
-//   probabilities are rounded to FP16 (2^-11 of each at most, the size of the output's own
-//   rounding), transposed by movmatrix into the B operand of O^T += V^T P^T.  Each warp keeps
+//   or fewer: E4M3 ragged 96 against 103 us; four of 64 bytes; one again where 16 query heads of
+//   128 fill the registers, so that two CTAs fit: 16 heads per key head, E4M3, 68 against 74 us):
+//   S^T = K Q^T as m16n8k16 MMAs with the keys as rows, so that 8 query heads fill the columns and no row is wasted on padding; the
+//   probabilities, times 2^14, are rounded to FP16 (2^-11 of each, the size of the output's own
+//   rounding, down to 2^-28 of the largest), transposed by movmatrix into the B operand of O^T += V^T P^T.  Each warp keeps
 //   its own m, l and O; they meet once per piece of a run.
 // * E4M3 entries become FP16 in registers (exactly); the per-head scales go into the score
 //   scale and the output.  The contraction indices are taken in the order in which the bytes
@@ -46,6 +46,11 @@ constexpr int kThreads = 32 * (kWarps + 1);
 // Parts of an item that one CTA adds up at once; more go in groups.  (131072 keys, 8 heads, 56
 // parts: 87.9 us in groups, 92.8 us at once; 1024 keys, 16 parts: 10.4 against 9.0 us.)
 constexpr int kFlatParts = 20;
+// Probabilities, their sum l and the weighted values are held times 2^kLift: a probability of the
+// maximum is 2^14 in FP16 (whose largest value is almost 2^16), and one that falls below FP16's
+// normal range is under 2^-28 of the maximum, where its rounding of 2^-39 is lost on no context
+// (unlifted, 2^-25 for each of 131072 keys could add up to 2^-8).
+constexpr float kLift = 14.f;
 
 template <int D, int kType, int NT>
 struct Cfg {
@@ -510,7 +515,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kType, NT>::kCtas) attention_
                         }
                     }
                     // (a maximum of -infinity, every score being one: 2^(-inf - 0) = 0)
-                    const float s0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], s1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+                    const float s0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] - kLift;
+                    const float s1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - kLift;
 #pragma unroll
                     for (int j = 0; j < kBlk; j++) {
                         const float p0 = exp2_fast(z[j][nt][0] - s0), p1 = exp2_fast(z[j][nt][1] - s1);
@@ -629,8 +635,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kType, NT>::kCtas) attention_
             if (!p.lse || warp != 0 || gid != 0) return;
             const int qi = nt * 8 + 2 * tig;
             float *at = p.lse + (int64_t)b * p.Hq + head0 + qi;
-            if (qi < nq) at[0] = lt.x == 0.f ? -INFINITY : 0.69314718055994530942f * (top.x + log2f(lt.x));
-            if (qi + 1 < nq) at[1] = lt.y == 0.f ? -INFINITY : 0.69314718055994530942f * (top.y + log2f(lt.y));
+            if (qi < nq) at[0] = lt.x == 0.f ? -INFINITY : 0.69314718055994530942f * (top.x + (log2f(lt.x) - kLift));
+            if (qi + 1 < nq) at[1] = lt.y == 0.f ? -INFINITY : 0.69314718055994530942f * (top.y + (log2f(lt.y) - kLift));
         };
         if (s.bad && warp == 0 && lane == 0) atomicOr(p.status, kDevStatusCacheRange);
         auto total_at = [&](int nt, int j) {

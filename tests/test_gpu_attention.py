@@ -235,3 +235,41 @@ def test_attention_scores_of_minus_infinity(bz):
                                                  D ** -0.5)
     assert (np.abs(got[1:2, :2] - want[:, :2]) <= tol[:, :2]).all()
     assert (np.abs(lse[1:2, :2] - want_lse[:, :2]) <= lse_tol[:, :2]).all()
+
+
+@pytest.mark.parametrize("kv", [0, 1])
+@pytest.mark.parametrize("heads", [1, 16])
+def test_attention_of_many_small_probabilities(bz, kv, heads):
+    """One key far above 32767 equal ones, whose probabilities of 2^-24.6 make up the result: each is
+    rounded by 2^-11 of itself (all alike, so the roundings do not cancel) and the output once more."""
+    import torch
+    D, page, n, z = 64, 64, 32768, 17.0625
+    kind = torch.float8_e4m3fn if kv else torch.float16
+    k = torch.zeros((n // page, 1, page, D), device="cuda")
+    k[0, 0, 0, 0] = 1
+    v = torch.ones_like(k)
+    v[0, 0, 0] = 0
+    one = torch.ones(1, device="cuda") if kv else None
+    q = np.zeros((1, heads, D), np.float16)
+    q[:, :, 0] = z
+    table = torch.arange(n // page, dtype=torch.int32, device="cuda")[None]
+    got, lse = run(bz, q, [k.to(kind), v.to(kind), one, one, table, torch.tensor([n], dtype=torch.int32, device="cuda")],
+                   heads, scale=1.0)
+    tail = (n - 1) * np.exp(-z)
+    want = tail / (1 + tail)
+    assert (np.abs(got - want) <= want * (2 * 2.0 ** -11 + 2.0 ** -19)).all(), (got.min(), got.max(), want)
+    assert (np.abs(lse - (z + np.log1p(tail))) <= 2.0 ** -19 * z).all()
+
+
+def test_attention_of_fewer_sequences_than_rows(bz):
+    """Matrices with more rows than the batch (padded buffers): the first rows are the batch's."""
+    import torch
+    rng = np.random.default_rng(16)
+    lengths, Hq, Hkv, D, page = [70, 5], 4, 2, 64, 16
+    pool = ref.Pool(rng, lengths, Hkv, D, page, 0)
+    q = rng.normal(0, 2, (8, Hq, D)).astype(np.float16)
+    out = torch.full((8, Hq * D), 3.0, dtype=torch.float16, device="cuda")
+    bz.bonsai_paged_attention(f16(q.reshape(8, -1)), *pool.device(), out, 2, Hq)
+    got = to_numpy_f16(out).reshape(8, Hq, D)
+    check(got[:2], None, q[:2], pool, 0, D ** -0.5)
+    assert (got[2:] == 3).all()
