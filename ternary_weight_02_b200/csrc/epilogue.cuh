@@ -44,7 +44,7 @@ __device__ __forceinline__ float gelu_erf(float z) {
     c = fmaf(c, t, 0.5f * -0.284496736f);
     c = fmaf(c, t, 0.5f * 0.254829592f);
     const float h = z * (c * t * exp2_unit(z * z * (-0.5f * kLog2E)));  // z erfc(x) / 2
-    return z < 0.f ? h : z - h;
+    return z < 0.f ? h : z - (z < INFINITY ? h : 0.f);  // (at +infinity h is infinity times 0)
 }
 
 // A NaN stays a NaN in every branch (the marker of a wait that gave up must not be lost).

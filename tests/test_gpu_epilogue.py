@@ -158,3 +158,24 @@ def test_forced_timeouts_reach_the_output(bz, M, N, K, algo):
     assert bz.bonsai_device_status(clear=True) != 0
     check(run(bz, p, dev, bias, residual, 1, algo), p.oracle_y(), bias, residual, 1)
     assert bz.bonsai_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("algo", [SIMPLE, GEMV, SKINNY, GEMM])
+@pytest.mark.parametrize("act", range(5))
+def test_infinite_sums(bz, act, algo):
+    """A bias of +-infinity gives the activation's value there (0 times infinity is a NaN); its
+    neighbours are what they are without it."""
+    import warnings
+    p = Problem(1, 300, 512, PQ2, seed=41)
+    dev = p.device()
+    bias, _ = inputs_of(p, 42)
+    plain = run(bz, p, dev, bias, None, act, algo)
+    bias[[5, 299]], bias[[6, 17]] = np.inf, -np.inf
+    got = run(bz, p, dev, bias, None, act, algo)
+    with warnings.catch_warnings():
+        warnings.simplefilter("ignore")
+        up, down = float(ref.activate(np.array([np.inf]), act)[0]), float(ref.activate(np.array([-np.inf]), act)[0])
+    assert up == np.inf and (got[0, [5, 299]] == np.inf).all()
+    assert np.array_equal(got[0, [6, 17]], [down, down], equal_nan=True)
+    others = np.setdiff1d(np.arange(300), [5, 6, 17, 299])
+    assert np.array_equal(got[0, others], plain[0, others])
