@@ -205,6 +205,8 @@ __global__ void __launch_bounds__(kMaxThreads) rope_kernel(Job job) {
                 sc[j] = __ldcg((k.head < job.H ? job.c.k_scale : job.c.v_scale) + kv_head(k));
         }
     };
+    int64_t slot = 0;  // (on its way before the values: the barrier below waits for it)
+    if (kMode != 0 && (int)threadIdx.x < nt) slot = __ldcg(job.slots + t0 + threadIdx.x);
     load(0);
     for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
         const int token = i / half;
@@ -222,7 +224,6 @@ __global__ void __launch_bounds__(kMaxThreads) rope_kernel(Job job) {
     // row of the tokens' entries in the pools' first head (or -1), in rows of D elements
     __shared__ int64_t entry[kMaxTokens];
     if (kMode != 0 && (int)threadIdx.x < nt) {
-        const int64_t slot = __ldcg(job.slots + t0 + threadIdx.x);
         if (slot >= job.c.pages * job.c.page_size) atomicOr(job.status, kDevStatusCacheRange);
         const bool in = slot >= 0 && slot < job.c.pages * job.c.page_size;
         entry[threadIdx.x] = in ? (((slot >> job.page_shift) * job.c.kv_heads) << job.page_shift) + (slot & (job.c.page_size - 1)) : -1;
