@@ -903,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tcgen05_kernel(
                                    (int64_t)tn * BN + half * 128, N, lane);
             // kEpi: the tile's later pieces are those of the next `later` CTAs; the warp waits for 32
             // flags at a time, a lane looking at each (in turn, five flags cost 4 us though all
-            // were up)
+            // were up; the __syncwarp ahead of each chunk's reads puts them behind every look)
             const int later = kEpi && owner ? (int)(((int64_t)tile_end * nunits - 1) / Ur) - unit : 0;
             if constexpr (kEpi) {
                 for (int k0 = 0; k0 < later; k0 += 32) {  // (the same trips in every lane: the wait votes)
