@@ -205,7 +205,9 @@ __global__ void __launch_bounds__(kMaxThreads) rope_kernel(Job job) {
                 sc[j] = __ldcg((k.head < job.H ? job.c.k_scale : job.c.v_scale) + kv_head(k));
         }
     };
-    int64_t slot = 0;  // (on its way before the values: the barrier below waits for it)
+    // the slots first, the barrier below waits for them (4096 tokens of 448 tasks: 24.3 us, 27.5
+    // with the slots behind the turns)
+    int64_t slot = 0;
     if (kMode != 0 && (int)threadIdx.x < nt) slot = __ldcg(job.slots + t0 + threadIdx.x);
     load(0);
     for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
