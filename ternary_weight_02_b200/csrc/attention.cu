@@ -31,6 +31,11 @@
 // * A (sequence, head) that spans CTAs leaves partial (m, l, O) in the workspace; the CTA that
 //   arrives last adds them up in run order (repeatable), so no CTA waits for another.
 //
+// Waits are bounded.  A consumer warp whose copy never lands gives up: its pieces become NaN, the
+// status bit is set, the joins run as ever, so that their counters end at zero.  The producer, whose
+// stages are then never freed, gives up too; and it leaves only when every copy that it started has
+// landed, since a copy must not outlive its CTA's shared memory.
+//
 // Keys outside the sequence's window get a score of -infinity, and their values are masked to
 // zero in the MMA operand (a NaN there times a zero probability would be a NaN).
 
@@ -95,6 +100,8 @@ struct Params {
     int B, Hq, Hkv, G, GT;                      // GT: query tiles of a key/value head
     int pages, page_shift;
     float scale;
+    uint32_t wait_limit;  // polls of the ring's waits
+    bool force_timeouts;  // test hook: the consumers wait for a copy that nobody makes
 };
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z, int w) {
@@ -230,11 +237,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kType, NT>::kCtas) attention_
     volatile int *bad_page = reinterpret_cast<int *>(empty + C::kStages);
     __shared__ int64_t scan_warp[kWarps + 1], start_off;
     __shared__ int start_b, start_len, last_flag;
+    __shared__ uint64_t never;  // a barrier that nobody arrives on
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gid = lane >> 2, tig = lane & 3;
     if (tid == 0) {
         for (int i = 0; i < C::kStages; i++) mbar_init(full + i, 1), mbar_init(empty + i, kWarps);
+        mbar_init(&never, 1);
         mbar_init_fence();
     }
     pdl_launch_dependents();
@@ -290,6 +299,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kType, NT>::kCtas) attention_
         const int slabs = kTile / slab;  // boxes of a tile and pool
         int st = 0, issued = 0;
         uint32_t phase = 1;  // the first pass over the ring finds every stage empty
+        // every stage's last copy has landed (the consumers may have given up on it)
+        auto drain = [&]() {
+            for (int i = issued < C::kStages ? 0 : issued - C::kStages; i < issued; i++)
+                mbar_wait(full + i % C::kStages, (uint32_t)(i / C::kStages) & 1u);
+        };
         while (walk.left > 0) {
             const int end = walk.end();
             const int hk = walk.hg / p.GT;
@@ -310,10 +324,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kType, NT>::kCtas) attention_
                     ids = ahead;
                     ahead = page_of(n + 32 + lane);
                 }
-                if (!__all_sync(0xffffffffu, mbar_wait(empty + st, phase))) {
-                    // the consumers gave up: let the copies in flight land, then leave
-                    for (int i = issued < C::kStages ? 0 : issued - C::kStages; i < issued; i++)
-                        mbar_wait(full + i % C::kStages, (uint32_t)(i / C::kStages) & 1u);
+                if (!__all_sync(0xffffffffu, mbar_wait(empty + st, phase, p.wait_limit))) {  // the consumers gave up
+                    drain();
                     return;
                 }
                 int valid = 0, bad = 0;
@@ -342,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kType, NT>::kCtas) attention_
             }
             walk.next(p, end);
         }
+        drain();
         return;
     }
 
@@ -411,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kType, NT>::kCtas) attention_
         }
         bool nan = s.bad;
         for (int t = walk.t; t < end; t++) {
-            if (alive && !mbar_wait(full + st, phase)) {
+            if (alive && !mbar_wait(p.force_timeouts ? &never : full + st, p.force_timeouts ? 0 : phase, p.wait_limit)) {
                 alive = false;
                 if (lane == 0) atomicOr(p.status, kDevStatusAttentionTimeout);
             }
@@ -866,6 +879,8 @@ cudaError_t launch_paged_attention(const uint16_t *q, const KvCache &c, const in
     p.pages = (int)c.pages;
     while ((1 << p.page_shift) < c.page_size) p.page_shift++;
     p.scale = scale;
+    p.force_timeouts = dev.force_wait_timeouts;
+    p.wait_limit = dev.force_wait_timeouts ? kForcedWaitPolls : kSpinLimit;
     auto by_queries = [&](auto one, auto two) { return G > 8 ? two(p, c, s, dev) : one(p, c, s, dev); };
     if (c.type == 0)
         return c.head_dim == 64    ? by_queries(launch<64, 0, 1>, launch<64, 0, 2>)
