@@ -270,7 +270,7 @@ int bonsai_rope_frequencies(double *freqs, double *magnitude, int64_t R, double 
  * sine and cosine and the products in FP32, one rounding to FP16.  x and out hold T rows of
  * H heads of D FP16 elements; row t starts at element t * ld_x (t * ld_out), so that the
  * query and key heads of a fused projection's output are rotated where they lie.  out may
- * be x with ld_out = ld_x (in place) but must not overlap it otherwise; elements between
+ * be x with ld_out = ld_x (in place; one row has no stride) but must not overlap it otherwise; elements between
  * H * D and the row stride are not touched.  freqs: R/2 FP64 values, positions: T int32
  * values, both device memory aligned to their element.  D a positive multiple of 8 up to
  * 1024; R even, 0 <= R <= D (R = 0 copies; freqs may then be NULL); ld_x and ld_out at least
@@ -302,7 +302,8 @@ typedef enum {
  * +-448 (a NaN stays one).  A negative slot writes no cache entry (a padded row); a slot of
  * pages * page_size or more writes none either and sets BONSAI_DEVICE_CACHE_RANGE in the
  * device status word.  Two tokens of one call must not share a slot.  q_out may be qkv with
- * ld_q = ld_qkv (the query heads then rotated in place) but must not overlap it otherwise.
+ * ld_q = ld_qkv (the query heads then rotated in place; one row has no stride) but must not
+ * overlap it otherwise.
  * Hq >= 0, a multiple of Hkv; ld_qkv >= (Hq + 2 Hkv) * D and ld_q >= Hq * D, multiples of
  * 8; positions (int32), slots (int64), freqs (FP64) and the scales aligned to their
  * element.  freqs, R, magnitude and layout as for bonsai_rope.  Uses the control words of

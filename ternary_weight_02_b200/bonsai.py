@@ -292,7 +292,9 @@ def _rows(t, rows: int, width: int, ld, dev: int):
         if ld is None:  # a matrix's rows may be wider, or more, than the call takes
             n = t.numel()
             if t.dim() == 2 and t.shape[1] >= width:
-                ld = t.shape[1]
+                # (one row of a wider matrix counts as contiguous: its stride is the matrix's, unless it
+                # is one that no rows can have)
+                ld = t.stride(0) if t.stride(0) >= width and t.stride(0) % 8 == 0 else t.shape[1]
             elif n == rows * width or rows == 0:
                 ld = width
             elif t.dim() > 1 and t.shape[0] == rows and n > rows * width:

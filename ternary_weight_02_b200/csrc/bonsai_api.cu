@@ -523,7 +523,7 @@ int bonsai_rope(const uint16_t *x, uint16_t *out, const double *freqs, const int
         R % 2 != 0 || R > D)
         return BONSAI_ERR_SHAPE;
     if (!row_stride_ok(ld_x, H * D) || !row_stride_ok(ld_out, H * D)) return BONSAI_ERR_SHAPE;
-    if (x != nullptr && x == out && ld_x != ld_out) return BONSAI_ERR_SHAPE;  // in place: the same rows
+    if (T > 1 && x != nullptr && x == out && ld_x != ld_out) return BONSAI_ERR_SHAPE;  // in place: the same rows
     if (T == 0 || H == 0) return BONSAI_OK;
     if (!x || !out || !positions || (R > 0 && !freqs)) return BONSAI_ERR_NULL;
     if (!aligned16(x) || !aligned16(out) || !aligned_to(freqs, 8) || !aligned_to(positions, 4)) return BONSAI_ERR_ALIGN;
@@ -545,7 +545,7 @@ int bonsai_rope_append(const uint16_t *qkv, uint16_t *q_out, void *k_cache, void
     if (rc != BONSAI_OK) return rc;
     if (T < 0 || T > kMaxDim || R < 0 || R % 2 != 0 || R > D) return BONSAI_ERR_SHAPE;
     if (!row_stride_ok(ld_qkv, (Hq + 2 * Hkv) * D) || !row_stride_ok(ld_q, Hq * D)) return BONSAI_ERR_SHAPE;
-    if (Hq > 0 && qkv != nullptr && qkv == q_out && ld_qkv != ld_q) return BONSAI_ERR_SHAPE;
+    if (T > 1 && Hq > 0 && qkv != nullptr && qkv == q_out && ld_qkv != ld_q) return BONSAI_ERR_SHAPE;
     if (T == 0) return BONSAI_OK;
     if (!qkv || (Hq > 0 && !q_out) || !k_cache || !v_cache || !positions || !slots || (R > 0 && !freqs))
         return BONSAI_ERR_NULL;
