@@ -225,7 +225,7 @@ typedef enum {
  * choose the kernel as in bonsai_ternary_linear_algo, except that the skinny kernel takes
  * batches of up to 1024 tokens here (in groups of 16), which the automatic choice
  * (BONSAI_ALGO_AUTO and 0) uses for small layers, and that the GEMM's CTA pairs
- * (split_k = 3) are not available and return BONSAI_ERR_ALGO.  An unknown act returns
+ * (split_k = 3) are not available and return BONSAI_ERR_ALGO, whoever chose the GEMM.  An unknown act returns
  * BONSAI_ERR_ARG.  A NaN sum (that of a wait that gave up, for instance) stays a
  * NaN through every activation.  The pages describe no such step: the projections of a decoder
  * layer add biases and the residual stream here. */

@@ -449,7 +449,7 @@ int bonsai_ternary_linear_epilogue(const uint16_t *x, const uint8_t *packed, con
         return BONSAI_ERR_ALIGN;
     int chosen = resolve_epilogue_algo(algo, M, N, K, fmt);
     if (chosen < 0) return chosen;
-    if (algo == BONSAI_ALGO_GEMM && split_k == 3) return BONSAI_ERR_ALGO;
+    if (algo == BONSAI_ALGO_GEMM && split_k == 3) return BONSAI_ERR_ALGO;  // (also without a device)
 
     std::lock_guard<std::mutex> lock(g_mutex);
     int dev;
@@ -457,6 +457,7 @@ int bonsai_ternary_linear_epilogue(const uint16_t *x, const uint8_t *packed, con
     rc = probe_current(&dev, &st);
     if (rc != BONSAI_OK) return rc;
     if (algo == BONSAI_ALGO_AUTO) chosen = resolve_epilogue_algo(algo, M, N, K, fmt, &st->info);
+    if (chosen == BONSAI_ALGO_GEMM && split_k == 3) return BONSAI_ERR_ALGO;
     if (chosen == BONSAI_ALGO_IMMA && !gemv_imma_grid_fits(N, K, st->info)) return BONSAI_ERR_ALGO;
     Workspace ws;
     rc = ensure_workspace(*st, workspace_for(chosen, M, N, K, fmt, split_k, st->info),
