@@ -226,7 +226,8 @@ typedef enum {
  * batches of up to 1024 tokens here (in groups of 16), which the automatic choice
  * (BONSAI_ALGO_AUTO and 0) uses for small layers, and that the GEMM's CTA pairs
  * (split_k = 3) are not available and return BONSAI_ERR_ALGO, whoever chose the GEMM.  An unknown act returns
- * BONSAI_ERR_ARG.  A NaN sum (that of a wait that gave up, for instance) stays a
+ * BONSAI_ERR_ARG.  The activations are FP32 (2^-20 relative for |z| up to 12; GELU's erfc to
+ * 1.5e-7 absolute, which near z = -4 is two half steps of FP16).  A NaN sum (that of a wait that gave up, for instance) stays a
  * NaN through every activation.  The pages describe no such step: the projections of a decoder
  * layer add biases and the residual stream here. */
 int bonsai_ternary_linear_epilogue(const uint16_t *x, const uint8_t *packed, const uint16_t *scales,
