@@ -16,9 +16,12 @@ CUDA graph.
   e2e        the same metric through the C ABI with pinned host buffers: every step
              copies the step's activations host -> device and its outputs back.
   cpu_baseline  the float64 CPU checker on a bounded sample (one layer), rank 0, N=1.
-  decode_layers  with --context L: one token through 64 whole decoder layers at a context of
-             L positions (qkv with bias, rotary positions and cache append, attention over the
-             paged cache, o with the residual, gate/up with SwiGLU, down with the residual).
+  decode_layers  with --context L: one token through what 64 decoder layers do between their
+             normalisations, at a context of L positions (qkv with bias, rotary positions and
+             cache append, attention over the paged cache, o with the residual, gate/up with
+             SwiGLU, down with the residual).  Without the normalisations the residual stream
+             would leave FP16's range in the third layer, so every layer starts from the same
+             input; all values are checked to be finite after the timed steps.
 
 Multi-GPU: one process per GPU (torchrun); each rank decodes its own token stream
 through its own copy of the stack (replicas, weak scaling, no collective on the
@@ -568,10 +571,13 @@ PREFILL_MS = (512, 2048, 8192)  # the prefill workload's token counts
 
 
 def measure_decode_layers(f, stack, bz, torch, stream, dev, args, hbm):
-    """One token through LAYERS decoder layers at a context of args.context positions: the
-    stack's projections with what lies between them (40 query and 8 key/value heads of 128,
-    the 7168 rows of qkv), each layer with its own FP16 cache in pages of 64.  Times the whole
-    step and the attention calls alone; bytes are the projections' and the cache's."""
+    """One token through LAYERS decoder layers, without their normalisations, at a context of
+    args.context positions: the stack's projections with what lies between them (40 query and 8
+    key/value heads of 128, the 7168 rows of qkv), each layer with its own FP16 cache in pages
+    of 64 and each from the same input x (an unnormalised stream through all of them would be
+    infinite from the third on, and the attention of NaN takes a path of its own).  Times the whole
+    step and the attention calls alone; bytes are the projections' and the cache's.  Raises
+    FloatingPointError if any value of the timed steps is not finite."""
     Hq, Hkv, D, page = 40, 8, 128, 64
     d, F, L = Hq * D, SHAPES[2][2] // 2, args.context
     width = (L + page - 1) // page
@@ -586,8 +592,9 @@ def measure_decode_layers(f, stack, bz, torch, stream, dev, args, hbm):
     freqs = freqs.to(dev)
     f16 = dict(dtype=torch.float16, device=dev)
     x, bias = torch.randn((1, d), generator=gen, **f16), torch.randn(SHAPES[0][2], generator=gen, **f16)
-    qkv, q, att, h = (torch.empty((1, n), **f16) for n in (SHAPES[0][2], d, d, F))
+    qkv, q, att, x1, h, x2 = (torch.empty((1, n), **f16) for n in (SHAPES[0][2], d, d, d, F, d))
     sp = stream.cuda_stream
+    torch.cuda.synchronize()  # (the inputs were made on another stream)
 
     def attend(layer):
         bz.bonsai_paged_attention(q, *pools[layer], None, None, table, lengths, att, 1, Hq, stream=sp)
@@ -599,9 +606,9 @@ def measure_decode_layers(f, stack, bz, torch, stream, dev, args, hbm):
             bz.bonsai_rope_append(qkv, q, *pools[layer], None, None, freqs, positions, slots, 1, Hq, D, magnitude=mag,
                                   stream=sp)
             attend(layer)
-            bz.bonsai_ternary_linear_epilogue(att, wo, so, None, x, x, 1, d, d, f, stream=sp)
-            bz.bonsai_ternary_linear_swiglu(x, wg, sg, h, 1, F, d, f, sp)
-            bz.bonsai_ternary_linear_epilogue(h, wd, sd, None, x, x, 1, d, F, f, stream=sp)
+            bz.bonsai_ternary_linear_epilogue(att, wo, so, None, x, x1, 1, d, d, f, stream=sp)
+            bz.bonsai_ternary_linear_swiglu(x1, wg, sg, h, 1, F, d, f, sp)
+            bz.bonsai_ternary_linear_epilogue(h, wd, sd, None, x1, x2, 1, d, F, f, stream=sp)
 
     def attention_only():
         for layer in range(LAYERS):
@@ -615,7 +622,20 @@ def measure_decode_layers(f, stack, bz, torch, stream, dev, args, hbm):
         out[name] = {"us": round(us, 2), "us_per_layer": round(us / LAYERS, 3), "gbs": round(nbytes / us / 1e3, 1),
                      "frac": round(nbytes / us / 1e3 / hbm, 4)}
         del g
-    return {"context": L, "packing": FMT_NAMES[f], "heads": [Hq, Hkv, D], **out}
+        torch.cuda.synchronize()
+        new = table[0, (L - 1) // page].long()  # the page of the appended entry
+        values = {"x": x, "qkv": qkv, "q": q, "attention": att, "x1": x1, "h": h, "x2": x2,
+                  "k_new": torch.stack([k[new, :, (L - 1) % page] for k, _ in pools]),
+                  "v_new": torch.stack([v[new, :, (L - 1) % page] for _, v in pools])}
+        out[name]["rms"] = {k: finite_rms(torch, k, v) for k, v in values.items()}
+    return {"context": L, "packing": FMT_NAMES[f], "heads": [Hq, Hkv, D], "normalisations": False, **out}
+
+
+def finite_rms(torch, name, values):
+    """Root mean square of a tensor whose values must all be finite."""
+    if not bool(torch.isfinite(values).all()):
+        raise FloatingPointError(f"{name} holds values that are not finite: the timed steps did not compute real data")
+    return round(float(values.double().square().mean().sqrt()), 4)
 
 
 def measure_prefill(fmt, base, dev, bz, torch, args, peaks, peak_kind):
@@ -788,7 +808,7 @@ def main():
                     help="token counts of the prefill grid (comma-separated)")
     ap.add_argument("--skinny", type=int, default=1, help="measure the M = 1..16 decode grid (PQ2_0, PTQ1_0)")
     ap.add_argument("--context", type=int, default=0,
-                    help="also measure whole decoder layers at this context length (0: no)")
+                    help="also measure decoder layers without their normalisations at this context length (0: no)")
     ap.add_argument("--case", choices=["gemv", "imma", "gemm", "skinny"], help="run one projection only (profiler case)")
     ap.add_argument("--shape", choices=[n for n, _, _ in SHAPES], default="gate_up")
     ap.add_argument("--m", type=int, default=2048,
