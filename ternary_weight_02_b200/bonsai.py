@@ -6,7 +6,9 @@ kernels.  Tensors are torch CUDA tensors (torch is used for device memory and
 streams only); plain integers are accepted as device pointers too.
 
 Importing this module fails loudly if libbonsai.so has not been built: there is
-no CPU fallback.  Build with ``python -m ternary_weight_02_b200.build``.
+no CPU fallback.  Build with ``python -m ternary_weight_02_b200.build``.  The entry points
+that a decode step calls per layer go through a small extension module that the same build
+makes, or through ctypes (1 to 2 us more of host time a call) where it cannot be loaded.
 """
 from __future__ import annotations
 
@@ -111,9 +113,8 @@ for _name, (_res, _args) in _SIGS.items():
 
 try:
     from . import _bonsai_call as _call  # the per-layer entry points without ctypes' conversions
-except ImportError as e:
-    raise ImportError("_bonsai_call.so is missing or does not load; build it with "
-                      "`python -m ternary_weight_02_b200.build`") from e
+except ImportError:
+    _call = _lib  # the same functions of libbonsai.so
 
 
 class BonsaiError(RuntimeError):

@@ -5,7 +5,9 @@
 Each csrc/*.cu is compiled to an object under _build/ (in parallel, skipped when
 up to date) and linked with the static CUDA runtime into
 ternary_weight_02_b200/libbonsai.so.  csrc/pycall.c, the binding's fast call path, becomes
-the extension module _bonsai_call.so beside it (gcc and the Python headers).  No GPU needed.
+the extension module _bonsai_call.abi3.so beside it (gcc and the Python headers; Python's
+stable ABI, so that one file serves every CPython from 3.10 on); where that cannot be built,
+the binding makes the same calls through ctypes.  No GPU needed.
 """
 from __future__ import annotations
 
@@ -15,6 +17,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -23,7 +26,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbonsai.so")
 CALL_SRC = os.path.join(CSRC, "pycall.c")
-CALL = os.path.join(PKG, "_bonsai_call.so")
+CALL = os.path.join(PKG, "_bonsai_call.abi3.so")
 HEADER = os.path.join(ROOT, "include", "bonsai.h")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -73,16 +76,34 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
         os.replace(tmp, LIB)
-    if (force or not os.path.exists(CALL)
-            or os.path.getmtime(CALL) < max(os.path.getmtime(CALL_SRC), os.path.getmtime(HEADER))):
-        tmp = CALL + ".tmp"
-        cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], CALL_SRC,
-               "-o", tmp, "-L", PKG, "-l:libbonsai.so", "-Wl,-rpath,$ORIGIN"]
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if res.returncode != 0:
-            raise RuntimeError(f"building {os.path.basename(CALL)} failed:\n{res.stdout}\n{res.stderr}")
-        os.replace(tmp, CALL)
+    build_call(force)
     return LIB
+
+
+def build_call(force: bool = False) -> str | None:
+    """The extension module behind the per-layer entry points, or None (and a note) where there is
+    no C compiler or no Python headers: the binding does without it."""
+    old = os.path.join(PKG, "_bonsai_call.so")  # of builds for one interpreter; any other would load it too
+    if os.path.exists(old):
+        os.remove(old)
+    if (not force and os.path.exists(CALL)
+            and os.path.getmtime(CALL) >= max(os.path.getmtime(CALL_SRC), os.path.getmtime(HEADER))):
+        return CALL
+    tmp = CALL + ".tmp"
+    cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-DPy_LIMITED_API=0x030A0000", "-I",
+           sysconfig.get_paths()["include"], CALL_SRC, "-o", tmp, "-L", PKG, "-l:libbonsai.so", "-Wl,-rpath,$ORIGIN"]
+    try:
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        note = res.stderr if res.returncode != 0 else None
+    except OSError as e:
+        note = str(e)
+    if note is not None:
+        print(f"{os.path.basename(CALL)} not built (calls go through ctypes): {note}", file=sys.stderr)
+        if os.path.exists(CALL):
+            os.remove(CALL)  # it belongs to older sources
+        return None
+    os.replace(tmp, CALL)
+    return CALL
 
 
 if __name__ == "__main__":
