@@ -255,8 +255,9 @@ __device__ __noinline__ void join_chunks16(const float *partials, uint16_t *y, E
 // the (group, token) blocks into the staged layout (as the rotation pass does), counts
 // itself in the workspace's call counter (ctl) and requests its first weights; before
 // staging x' it waits (bounded) until the last CTA has advanced the counter.  The grid
-// is then resident at once (the launcher checks the occupancy).  If that wait gives up,
-// the CTA writes NaN and sets the status bit.
+// is then resident at once (the launcher checks the occupancy).  If that wait gives up
+// (after wait_limit polls; with force_timeouts, the test hook, whatever the counter says), the
+// CTA writes NaN and sets the status bit.
 //
 // kTma: the weights and scales come by TMA into a ring of kTStages stages per warp (the
 // warp's 16 rows x kTGroups groups, 128-byte swizzle; scales unswizzled), one mbarrier
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, (kEpi ? 2 : 0)) skinny_kernel(
     const uint16_t *__restrict__ scales, uint16_t *__restrict__ y, float *__restrict__ partials,
     unsigned int *__restrict__ counters, int M, int64_t N, int64_t K, int S, int gpc,
     const uint16_t *__restrict__ x, unsigned int *__restrict__ ctl, const __grid_constant__ CUtensorMap wmap,
-    const __grid_constant__ CUtensorMap smap, Epilogue epi) {
+    const __grid_constant__ CUtensorMap smap, Epilogue epi, uint32_t wait_limit, bool force_timeouts) {
     constexpr int MT = NT * 8;  // tokens padded
     static_assert(sub_groups<NT>() % kRing == 0, "ring slots follow the group index");
     static_assert(!kTma || (kFmt != 1 && sub_groups_tma<NT>() % kTGroups == 0), "TMA stages follow the group index");
@@ -450,14 +451,14 @@ __global__ void __launch_bounds__(kThreads, (kEpi ? 2 : 0)) skinny_kernel(
         if (tid == 0) {
             const uint32_t calls = (uint32_t)(arrival >> 32);
             uint32_t i = 0;
-            for (; i < kSpinLimit; i++) {
+            for (; i < wait_limit; i++) {
                 uint32_t hi;
                 asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(hi) : "l"(ctl + kCtlCalls + 1) : "memory");
-                if (hi != calls) break;
+                if (hi != calls && !force_timeouts) break;
                 __nanosleep(32);
             }
-            ok_s = i < kSpinLimit;
-            if (i == kSpinLimit) atomicOr(ctl + kCtlStatus, kDevStatusSkinnyTimeout);
+            ok_s = i < wait_limit;
+            if (i == wait_limit) atomicOr(ctl + kCtlStatus, kDevStatusSkinnyTimeout);
         }
         __syncthreads();
         barrier_ok = ok_s != 0;
@@ -843,7 +844,8 @@ cudaError_t launch(const uint16_t *x, const uint8_t *packed, const uint16_t *sca
             prep<<<dim3((unsigned)((G * MT + 7) / 8), (unsigned)token_groups(M)), 256, 0, s>>>(x, xsg, gsg, (int)M, K);
         kern<<<grid, kThreads, smem, s>>>(xsg, gsg, packed, scales, y, partials, ws.counters, (int)M, N, K, S, gpc,
                                           fused ? x : nullptr, reinterpret_cast<unsigned int *>(ws.zeroed), wmap,
-                                          smap, epi);
+                                          smap, epi, dev.force_wait_timeouts ? kForcedWaitPolls : kSpinLimit,
+                                          dev.force_wait_timeouts);
         return cudaGetLastError();
     };
     if (M <= 8) {
