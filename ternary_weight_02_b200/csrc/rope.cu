@@ -96,9 +96,8 @@ __device__ __forceinline__ uint4 load8(const uint16_t *row, int at, int n) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 template <bool kWhole>
-__device__ __forceinline__ void store8(uint16_t *row, int at, int n, const float (&v)[8]) {
+__device__ __forceinline__ void store8(uint16_t *row, int at, int n, const uint4 &u) {
     uint16_t *p = row + at;
-    const uint4 u = pack8(v);
     if (kWhole || (n == 8 && (at & 7) == 0)) {
         *reinterpret_cast<uint4 *>(p) = u;
         return;
@@ -235,6 +234,7 @@ __global__ void __launch_bounds__(kMaxThreads) rope_kernel(Job job) {
         float a[8], b[8];
         unpack8(c0, a);
         unpack8(c1, b);
+        uint4 u0 = c0, u1 = c1;  // what is not rotated keeps its bits, a NaN's too
         if (k.task >= 0) {
             const float4 *cs = reinterpret_cast<const float4 *>(turn + k.token * turn_stride) + k.task;
             float2 f[8];
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kMaxThreads) rope_kernel(Job job) {
                 auto rotate = [&](float (&v)[8], const float2 *g, int first) {  // pairs first .. of a chunk
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
-                        if (!kWhole && first + i >= half) continue;  // (elements that are not rotated)
+                        if (!kWhole && first + i >= half) continue;  // (elements that are not rotated, for an E4M3 entry)
                         const float p = v[2 * i], q = v[2 * i + 1];
                         v[2 * i] = p * g[i].x - q * g[i].y;
                         v[2 * i + 1] = q * g[i].x + p * g[i].y;
@@ -263,10 +263,21 @@ __global__ void __launch_bounds__(kMaxThreads) rope_kernel(Job job) {
                 rotate(a, f, 4 * k.task);
                 rotate(b, f + 4, 4 * (job.rot + k.task));
             }
+            u0 = pack8(a), u1 = pack8(b);
+            if (!kWhole && kLayout == 1) {
+                auto rest = [&](uint4 &u, const uint4 &c, int first) {  // pairs of the chunk past the rotated ones
+                    if (first + 0 >= half) u.x = c.x;
+                    if (first + 1 >= half) u.y = c.y;
+                    if (first + 2 >= half) u.z = c.z;
+                    if (first + 3 >= half) u.w = c.w;
+                };
+                rest(u0, c0, 4 * k.task);
+                rest(u1, c1, 4 * (job.rot + k.task));
+            }
         }
         auto put16 = [&](uint16_t *row) {
-            store8<kWhole>(row, k.at0, k.n0, a);
-            if (k.n1 > 0) store8<kWhole>(row, k.at1, k.n1, b);
+            store8<kWhole>(row, k.at0, k.n0, u0);
+            if (k.n1 > 0) store8<kWhole>(row, k.at1, k.n1, u1);
         };
         if (kMode == 0 || k.head < job.Hq) {
             put16(job.out + (t0 + k.token) * job.ld_out + (int64_t)k.head * job.D);
