@@ -57,9 +57,11 @@
  *     partials, an FP16 copy of x' for the prefill GEMM, the partial results of
  *     bonsai_paged_attention).  It is allocated
  *     with cudaMalloc on the first call that needs it, grown when a larger
- *     call arrives (after a device synchronisation), and released by
+ *     call arrives (with a device synchronisation), and released by
  *     bonsai_shutdown().  Calls that use it must not overlap on the GPU (keep
  *     them on one stream); bonsai_reserve() sizes it ahead of stream capture.
+ *     A workspace that a larger one replaces is kept until bonsai_shutdown(), so
+ *     that captured calls stay valid; replay none after it.
  *   - Invalid codes in a packed plane (PTQ1_0 bytes >= 243, PQ2_0 code 3)
  *     produce unspecified output values but never out-of-bounds accesses.
  *   - Every wait inside a kernel (a barrier on a copy in flight, a hand-over

@@ -8,6 +8,7 @@
 
 #include <cmath>
 #include <mutex>
+#include <vector>
 
 #include "../../include/bonsai.h"
 #include "common.cuh"
@@ -30,6 +31,8 @@ struct DeviceState {
     size_t ws_bytes = 0;  // total allocation (counters + data)
     void *zb_base = nullptr;
     size_t zb_bytes = 0;  // the zero-initialised region
+    // buffers that larger ones took the place of: captured calls still use them
+    std::vector<void *> old_ws, old_zb;
 };
 
 std::mutex g_mutex;
@@ -65,53 +68,54 @@ int probe_current(int *dev_out, DeviceState **st_out) {
     return st.status;
 }
 
+// Puts a buffer of at least `need` bytes, at least half as large again as the one it replaces
+// (so that all replaced ones together hold about twice its bytes at most), in the place of
+// *base, its first `zeroed` bytes (0: all) zero.  The old buffer stays, in `old`: captured
+// calls hold its address, and work in flight may use it.
+int grow_buffer(void **base, size_t *bytes, std::vector<void *> *old, size_t need, size_t zeroed) {
+    try {
+        old->reserve(old->size() + 1);
+    } catch (...) {  // no exception leaves a C entry point
+        return BONSAI_ERR_NOMEM;
+    }
+    size_t size = *bytes + *bytes / 2 > need ? *bytes + *bytes / 2 : need;
+    void *p = nullptr;
+    cudaError_t e = cudaMalloc(&p, size);
+    if (e != cudaSuccess && size > need) {
+        cudaGetLastError();
+        size = need;
+        e = cudaMalloc(&p, size);
+    }
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return BONSAI_ERR_NOMEM;
+    }
+    if (cudaMemset(p, 0, zeroed == 0 ? size : zeroed) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+        cudaFree(p);
+        return BONSAI_ERR_CUDA;
+    }
+    if (*base) old->push_back(*base);
+    *base = p;
+    *bytes = size;
+    return BONSAI_OK;
+}
+
 // Makes sure the current device's workspace holds at least data_bytes after the
-// counter block.  Grows by reallocating (after a device synchronisation, since
-// work in flight may still use the old buffer).
+// counter block.
 int ensure_workspace(DeviceState &st, size_t data_bytes, size_t zeroed_bytes, Workspace *ws) {
     const size_t need = kCounterBytes + ((data_bytes + 255) / 256) * 256;
     // the zeroed region always holds at least the control words (the device status word)
     if (zeroed_bytes < kCtlRegionBytes) zeroed_bytes = kCtlRegionBytes;
-    if (st.ws_bytes < need) {
-        if (st.ws_base) {
-            if (cudaDeviceSynchronize() != cudaSuccess) return BONSAI_ERR_CUDA;
-            cudaFree(st.ws_base);
-            st.ws_base = nullptr;
-            st.ws_bytes = 0;
-        }
-        size_t grow = need < (size_t(64) << 20) ? (size_t(64) << 20) : need;  // at least 64 MiB
-        void *p = nullptr;
-        if (cudaMalloc(&p, grow) != cudaSuccess) {
-            cudaGetLastError();
-            return BONSAI_ERR_NOMEM;
-        }
+    if (st.ws_bytes < need) {  // at least 64 MiB
         // counters must start at zero; the kernels keep them at zero afterwards
-        if (cudaMemset(p, 0, kCounterBytes) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
-            cudaFree(p);
-            return BONSAI_ERR_CUDA;
-        }
-        st.ws_base = p;
-        st.ws_bytes = grow;
+        const int rc = grow_buffer(&st.ws_base, &st.ws_bytes, &st.old_ws, need < (size_t(64) << 20) ? (size_t(64) << 20) : need,
+                                   kCounterBytes);
+        if (rc != BONSAI_OK) return rc;
     }
     if (st.zb_bytes < zeroed_bytes) {
-        if (st.zb_base) {
-            if (cudaDeviceSynchronize() != cudaSuccess) return BONSAI_ERR_CUDA;
-            cudaFree(st.zb_base);
-            st.zb_base = nullptr;
-            st.zb_bytes = 0;
-        }
-        const size_t grow = zeroed_bytes < (size_t(16) << 20) ? (size_t(16) << 20) : zeroed_bytes;
-        void *p = nullptr;
-        if (cudaMalloc(&p, grow) != cudaSuccess) {
-            cudaGetLastError();
-            return BONSAI_ERR_NOMEM;
-        }
-        if (cudaMemset(p, 0, grow) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
-            cudaFree(p);
-            return BONSAI_ERR_CUDA;
-        }
-        st.zb_base = p;
-        st.zb_bytes = grow;
+        const int rc = grow_buffer(&st.zb_base, &st.zb_bytes, &st.old_zb,
+                                   zeroed_bytes < (size_t(16) << 20) ? (size_t(16) << 20) : zeroed_bytes, 0);
+        if (rc != BONSAI_OK) return rc;
     }
     ws->zeroed = static_cast<uint8_t *>(st.zb_base);
     ws->zeroed_bytes = st.zb_bytes;
@@ -674,15 +678,18 @@ int bonsai_device_status(void *stream, uint32_t *bits, int clear) {
     if (rc != BONSAI_OK) return rc;
     if (!st->zb_base) return BONSAI_OK;  // no call has run on this device: nothing to report
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    unsigned int *word = static_cast<unsigned int *>(st->zb_base) + kCtlStatus;
-    unsigned int host = 0;
-    if (cudaMemcpyAsync(&host, word, sizeof(host), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        (clear && cudaMemsetAsync(word, 0, sizeof(unsigned int), s) != cudaSuccess) ||
-        cudaStreamSynchronize(s) != cudaSuccess) {
-        cudaGetLastError();
-        return BONSAI_ERR_CUDA;
+    // the status word, and those of calls captured before the region grew
+    for (size_t i = 0; i <= st->old_zb.size(); i++) {
+        unsigned int *word = static_cast<unsigned int *>(i == 0 ? st->zb_base : st->old_zb[i - 1]) + kCtlStatus;
+        unsigned int host = 0;
+        if (cudaMemcpyAsync(&host, word, sizeof(host), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+            (clear && cudaMemsetAsync(word, 0, sizeof(unsigned int), s) != cudaSuccess) ||
+            cudaStreamSynchronize(s) != cudaSuccess) {
+            cudaGetLastError();
+            return BONSAI_ERR_CUDA;
+        }
+        *bits |= host;
     }
-    *bits = host;
     return BONSAI_OK;
 }
 
@@ -697,20 +704,18 @@ void bonsai_shutdown(void) {
     int current = -1;
     cudaGetDevice(&current);
     for (int d = 0; d < kMaxDevices; d++) {
-        if (g_dev[d].ws_base) {
-            cudaSetDevice(d);
-            cudaDeviceSynchronize();
-            cudaFree(g_dev[d].ws_base);
-            g_dev[d].ws_base = nullptr;
-            g_dev[d].ws_bytes = 0;
-        }
-        if (g_dev[d].zb_base) {
-            cudaSetDevice(d);
-            cudaDeviceSynchronize();
-            cudaFree(g_dev[d].zb_base);
-            g_dev[d].zb_base = nullptr;
-            g_dev[d].zb_bytes = 0;
-        }
+        DeviceState &st = g_dev[d];
+        if (!st.ws_base && !st.zb_base) continue;
+        cudaSetDevice(d);
+        cudaDeviceSynchronize();
+        for (void *p : st.old_ws) cudaFree(p);
+        for (void *p : st.old_zb) cudaFree(p);
+        cudaFree(st.ws_base);  // (of a null pointer: nothing)
+        cudaFree(st.zb_base);
+        st.old_ws.clear();
+        st.old_zb.clear();
+        st.ws_base = st.zb_base = nullptr;
+        st.ws_bytes = st.zb_bytes = 0;
     }
     if (current >= 0) cudaSetDevice(current);
     cudaGetLastError();
