@@ -295,7 +295,9 @@ def _rows(t, rows: int, width: int, ld, dev: int):
             if t.dim() == 2 and t.shape[1] >= width:
                 # (one row of a wider matrix counts as contiguous: its stride is the matrix's, unless it
                 # is one that no rows can have)
-                ld = t.stride(0) if t.stride(0) >= width and t.stride(0) % 8 == 0 else t.shape[1]
+                ld = t.stride(0)
+                if ld < width or ld & 7:
+                    ld = t.shape[1]
             elif n == rows * width or rows == 0:
                 ld = width
             elif t.dim() > 1 and t.shape[0] == rows and n > rows * width:
