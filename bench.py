@@ -15,7 +15,7 @@ CUDA graph.
              its stream, against the measured HBM copy bandwidth.
   e2e        the same metric through the C ABI with pinned host buffers: every step
              copies the step's activations host -> device and its outputs back.
-  cpu_baseline  the float64 CPU checker on a bounded sample (one layer), rank 0, N=1.
+  cpu_baseline  the float64 CPU oracle on a bounded sample (one layer), rank 0, N=1.
   decode_layers  with --context L: one token through what 64 decoder layers do between their
              normalisations, at a context of L positions (qkv with bias, rotary positions and
              cache append, attention over the paged cache, o with the residual, gate/up with
@@ -25,7 +25,7 @@ CUDA graph.
 
 Multi-GPU: one process per GPU (torchrun); each rank decodes its own token stream
 through its own copy of the stack (replicas, weak scaling, no collective on the
-data path).  `--impl reference` times the CPU checker itself on the same metric.
+data path).  `--impl reference` times the CPU oracle itself on the same metric.
 """
 from __future__ import annotations
 
@@ -225,7 +225,7 @@ def kernel_traffic(fmt):
 # ------------------------------------------------------------------ reference arm
 
 def run_reference(args):
-    """The CPU checker as it stands, timed on this host's cores: each step is one layer
+    """The CPU oracle as it stands, timed on this host's cores: each step is one layer
     (the four projections) of the stack at M = 1, a bounded sample of the workload."""
     import oracle
     from ternary_weight_02_b200 import inputs
@@ -736,7 +736,7 @@ def measure_swiglu_prefill(fmt, base, dev, bz, torch, M, calls, flush):
 
 
 def cpu_baseline(fmt):
-    """The checker on one layer of the stack (rank 0, N = 1): a bounded CPU sample, timed
+    """The oracle on one layer of the stack (rank 0, N = 1): a bounded CPU sample, timed
     on all host cores and on one."""
     import oracle
     from ternary_weight_02_b200 import inputs

@@ -1,4 +1,4 @@
-"""Python face of the CPU checker (``bonsai_oracle.c``).
+"""Python face of the CPU oracle (``bonsai_oracle.c``).
 
 TEST INFRASTRUCTURE ONLY: the test suite, ``__graft_entry__.smoke()`` and the
 benchmark's CPU-baseline / reference leg are the only callers.  Nothing in the
@@ -36,7 +36,7 @@ def scale_group(fmt: int) -> int:
 
 
 def build(force: bool = False) -> str:
-    """Compile the checker with gcc (OpenMP on) unless an up-to-date build exists."""
+    """Compile the oracle with gcc (OpenMP on) unless an up-to-date build exists."""
     if (not force and os.path.exists(LIB)
             and os.path.getmtime(LIB) >= os.path.getmtime(SRC)):
         return LIB

@@ -1,5 +1,5 @@
 /*
- * bonsai_oracle.c -- plain CPU checker for the Bonsai 2 ternary linear layer.
+ * bonsai_oracle.c -- plain CPU oracle for the Bonsai 2 ternary linear layer.
  *
  * TEST INFRASTRUCTURE ONLY.  Only the test suite, the package smoke check and
  * the benchmark's CPU-baseline / reference leg may load this library.  The

@@ -3,7 +3,8 @@
 Every function has the name of the C entry point it calls and forwards raw
 device pointers, sizes and the CUDA stream; all computation happens in the CUDA
 kernels.  Tensors are torch CUDA tensors (torch is used for device memory and
-streams only); plain integers are accepted as device pointers too.
+streams only); plain integers are accepted as device pointers too, except for cache pools and
+page tables, whose shapes the binding reads.
 
 Importing this module fails loudly if libbonsai.so has not been built: there is
 no CPU fallback.  Build with ``python -m ternary_weight_02_b200.build``.  The entry points

@@ -190,8 +190,9 @@ int resolve_algo(int algo, int64_t M, int64_t N, int64_t K, int fmt, const Devic
 // As resolve_algo, for a call with an epilogue: the skinny kernel also takes larger batches there,
 // in groups of 16 tokens that re-read the weights (from the L2, mostly), and the automatic choice
 // compares the two kernels' estimated times.  PQ2_0, us, skinny in groups against GEMM:
-//   1001 x 1024:  M = 32 8.4 / 27, M = 1024 18 / 38;  5120 x 5120: M = 64 29 / 32, M = 128 45 / 33;
-//   5120 x 17408: M = 32 38 / 49, M = 64 88 / 51.
+//   1001 x 1024:  M = 32 8.3 / 27, M = 1024 19 / 38;  5120 x 5120: M = 64 30 / 34, M = 128 44 / 34;
+//   5120 x 17408: M = 32 39 / 50, M = 64 87 / 50;  and where the estimates choose the slower one:
+//   1024 x 4096:  M = 512 29 / 34 (the GEMM; g64 32.5 / 34.4).
 int resolve_epilogue_algo(int algo, int64_t M, int64_t N, int64_t K, int fmt, const DeviceInfo *dev = nullptr) {
     if (M > 16 && skinny_groups_supported(M, N, K, fmt)) {
         if (algo == BONSAI_ALGO_SKINNY) return algo;

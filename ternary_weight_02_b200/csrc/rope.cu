@@ -12,9 +12,10 @@
 // one head, two 16-byte loads and stores half the rotated part apart in both layouts
 // (neighbouring threads then move neighbouring 16 bytes).  When 8 pairs do not divide the
 // rotated part (R % 16 != 0, !kWhole) the last task has fewer, and in the half layout the
-// partners start inside a 16-byte chunk and move in words or halfwords.  8191 tokens of 48
-// heads of 128: 33.7 us, 5.98 TB/s (91% of the measured copy); with R = 126 interleaved 35.5,
-// half 95 us.
+// partners start inside a 16-byte chunk and move in words or halfwords.  What is not rotated is
+// moved as it is, bits untouched.  8191 tokens of 48 heads of 128, device time in a graph of such
+// calls: interleaved 32.1 us, 6.3 TB/s (96% of the measured copy), half 34.3 us (90%); with
+// R = 126 interleaved 34.8, half 95 us.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -204,8 +205,8 @@ __global__ void __launch_bounds__(kMaxThreads) rope_kernel(Job job) {
                 sc[j] = __ldcg((k.head < job.H ? job.c.k_scale : job.c.v_scale) + kv_head(k));
         }
     };
-    // the slots first, the barrier below waits for them (4096 tokens of 448 tasks: 24.3 us, 27.5
-    // with the slots behind the turns)
+    // the slots first, the barrier below waits for them (4096 tokens of 448 tasks: 23.9 us, 26.6
+    // with the slots behind the turns; E4M3 25.8 and 28.7)
     int64_t slot = 0;
     if (kMode != 0 && (int)threadIdx.x < nt) slot = __ldcg(job.slots + t0 + threadIdx.x);
     load(0);
@@ -327,9 +328,9 @@ cudaError_t launch(Job &job, cudaStream_t s, const DeviceInfo &dev) {
     tokens = tokens < spread ? tokens : spread;
     tokens = tokens < 1 ? 1 : tokens > kMaxTokens ? kMaxTokens : tokens;
     job.tokens = (int)tokens;
-    // Few tokens: every task its own thread (32 tokens of 448 tasks: 3.3 us with 512 threads, 4.9
+    // Few tokens: every task its own thread (32 tokens of 448 tasks: 2.9 us with 512 threads, 4.3
     // with 128).  Many: four tasks per thread keep more loads in flight per CTA and fewer warps at
-    // its barrier (8191 tokens of 384 tasks: 41 us with 128 threads, 50 with 256).
+    // its barrier (8191 tokens of 384 tasks: 34.3 us with 128 threads, 39.3 with 256).
     int64_t threads = job.T < 2 * (int64_t)dev.sm_count ? per_token * tokens : 128;
     threads = threads > kMaxThreads ? kMaxThreads : threads < 64 ? 64 : (threads + 31) / 32 * 32;
     job.head_shift = -1;

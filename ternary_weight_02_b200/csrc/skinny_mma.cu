@@ -50,8 +50,8 @@
 // * Calls with an epilogue (kEpi: bias, activation, residual on the FP32 sums) take larger
 //   batches too, as grid slices of 16 tokens that re-read the weights through the L2: the
 //   batch-independent cost of the GEMM (rotation, grid barrier, hand-over of split tiles: 20
-//   to 60 us) is more than that for small layers.  1001 x 1024, PQ2_0, M = 128: 8 us
-//   against 46; the choice is made by the two kernels' estimated times.
+//   to 60 us) is more than that for small layers.  1001 x 1024, PQ2_0, M = 128: 8.6 us
+//   against 37.5; the choice is made by the two kernels' estimated times.
 #include <cstring>
 
 #include "common.cuh"

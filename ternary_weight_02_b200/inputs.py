@@ -2,7 +2,7 @@
 
 This module draws random numbers and nothing else: it holds none of the
 layer's arithmetic (no packing, no Hadamard transform, no dot product).
-Both the CUDA path and the CPU checker are fed from it.
+Both the CUDA path and the CPU oracle are fed from it.
 
 Generator: SplitMix64 (Steele, Lea & Flood, "Fast splittable pseudorandom
 number generators", OOPSLA 2014) used as a counter-based generator.  The
