@@ -412,7 +412,7 @@ int bonsai_device_status(void *stream, uint32_t *bits, int clear);
  * flags, look for a call number that no CTA writes and give up after 64 polls; so does the
  * skinny kernel's wait after its rotation phase, whatever has arrived, and those of
  * bonsai_paged_attention wait as long for a copy that nobody makes.  The calls
- * then write NaN for those tiles (the last two: everywhere) and set the status bits, without any
+ * then write NaN for those tiles (the last two: everywhere but for sequences without keys) and set the status bits, without any
  * fault, so that the timeout path can be tested.  Off by default; applies to calls launched while enabled. */
 int bonsai_debug_force_timeouts(int enable);
 
