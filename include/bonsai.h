@@ -227,10 +227,10 @@ typedef enum {
  * choose the kernel as in bonsai_ternary_linear_algo, except that the skinny kernel takes
  * batches of up to 1024 tokens here (in groups of 16), which the automatic choice
  * (BONSAI_ALGO_AUTO and 0) uses for small layers, and that the GEMM's CTA pairs
- * (split_k = 3) are not available and return BONSAI_ERR_ALGO, whoever chose the GEMM.  An unknown act returns
- * BONSAI_ERR_ARG.  The activations are FP32 (2^-20 relative for |z| up to 12; GELU's erfc to
- * 1.5e-7 absolute, which near z = -4 is two half steps of FP16).  A NaN sum (that of a wait that gave up, for instance) stays a
- * NaN through every activation.  The pages describe no such step: the projections of a decoder
+ * (split_k = 3) are not available and return BONSAI_ERR_ALGO, whoever chose the GEMM.  An
+ * unknown act returns BONSAI_ERR_ARG.  The activations are computed in FP32; GELU's erfc is off by
+ * up to 1.5e-7, which near z = -4 comes to 1.25 half steps of FP16 ahead of the rounding.  A NaN
+ * sum (that of a wait that gave up, for instance) stays a NaN through every activation.  The pages describe no such step: the projections of a decoder
  * layer add biases and the residual stream here. */
 int bonsai_ternary_linear_epilogue(const uint16_t *x, const uint8_t *packed, const uint16_t *scales,
                                    const uint16_t *bias, const uint16_t *residual, uint16_t *y, int64_t M,
@@ -273,8 +273,8 @@ int bonsai_rope_frequencies(double *freqs, double *magnitude, int64_t R, double 
  * sine and cosine and the products in FP32, one rounding to FP16.  x and out hold T rows of
  * H heads of D FP16 elements; row t starts at element t * ld_x (t * ld_out), so that the
  * query and key heads of a fused projection's output are rotated where they lie.  out may
- * be x with ld_out = ld_x (in place; one row has no stride) but must not overlap it otherwise; elements between
- * H * D and the row stride are not touched.  freqs: R/2 FP64 values, positions: T int32
+ * be x with ld_out = ld_x (in place; one row has no stride) but must not overlap it otherwise;
+ * elements between H * D and the row stride are not touched.  freqs: R/2 FP64 values, positions: T int32
  * values, both device memory aligned to their element.  D a positive multiple of 8 up to
  * 1024; R even, 0 <= R <= D (R = 0 copies; freqs may then be NULL); ld_x and ld_out at least
  * H * D and multiples of 8.  No workspace. */
@@ -334,8 +334,8 @@ int bonsai_rope_append(const uint16_t *qkv, uint16_t *q_out, void *k_cache, void
  * that is negative or exceeds max_pages * page_size, makes that sequence's outputs NaN and
  * sets BONSAI_DEVICE_CACHE_RANGE; nothing outside the buffers is read.
  *   Statistics, scores and sums are FP32; the probabilities are rounded to FP16 before the
- * product with the values (2^-11 of each; below 2^-28 of a sequence's largest, 2^-39 of that).  Results depend on the lengths and the device's SM count only
- * (bitwise repeatable).  Hq a positive multiple of Hkv; ld_q, ld_out at least Hq * D and
+ * product with the values (2^-11 of each; below 2^-28 of a sequence's largest, 2^-39 of that).
+ * Results depend on the lengths and the device's SM count only (bitwise repeatable).  Hq a positive multiple of Hkv; ld_q, ld_out at least Hq * D and
  * multiples of 8; page_table, lengths, lse and the scales aligned to their element; window
  * >= 0.  Uses the workspace: see the conventions above (less of it than bonsai_reserve makes
  * for any shape). */
@@ -412,8 +412,9 @@ int bonsai_device_status(void *stream, uint32_t *bits, int clear);
  * flags, look for a call number that no CTA writes and give up after 64 polls; so does the
  * skinny kernel's wait after its rotation phase, whatever has arrived, and those of
  * bonsai_paged_attention wait as long for a copy that nobody makes.  The calls
- * then write NaN for those tiles (the last two: everywhere but for sequences without keys) and set the status bits, without any
- * fault, so that the timeout path can be tested.  Off by default; applies to calls launched while enabled. */
+ * then write NaN for those tiles (the last two: everywhere but for sequences without keys) and
+ * set the status bits, without any fault, so that the timeout path can be tested.  Off by default;
+ * applies to calls launched while enabled. */
 int bonsai_debug_force_timeouts(int enable);
 
 /* Frees the workspaces of every device (after synchronising each).  The
